@@ -42,31 +42,31 @@ def listed():
     M, V = 8192 * 2048, 2048  # a 2B layer's FFN matrix and norm vector
     return [
         # one decoded token between two layers of the 2B shape: the smallest call
-        _norm("norm fwd, 1 token", False, 1, 2048),
+        _norm("norm fwd 1 token", False, 1, 2048),
         # the prefill batch of the 2B shape, fp32 residual stream
-        _norm("norm fwd, 16384 tokens", False, 16384, 2048),
+        _norm("norm fwd 16384 tokens", False, 16384, 2048),
         # the training batch of the 2B shape, one gate vector (a learned per-channel scale)
-        _norm("norm bwd, 8192 tokens", True, 8192, 2048, group=8192, block=0.5),
+        _norm("norm bwd 8192 tokens", True, 8192, 2048, group=8192, block=0.5),
         # ragged: 5 sequences of up to 700 tokens with a gate row each, bf16 residual stream, odd width
-        _norm("norm bwd, 5 gated sequences", True, 3301, 1000, r="bf16", group=700, res=0.9),
+        _norm("norm bwd 5 gated sequences", True, 3301, 1000, r="bf16", group=700, res=0.9),
         # one decoded token, 2B weights: bound by reading the weights once
-        _ffn("ffn fwd, 1 token", False, 1, 2048, 8192, "silu"),
+        _ffn("ffn fwd 1 token", False, 1, 2048, 8192, "silu"),
         # a decoding batch of odd size
-        _ffn("ffn fwd, 37 tokens", False, 37, 2048, 8192, "gelu"),
+        _ffn("ffn fwd 37 tokens", False, 37, 2048, 8192, "gelu"),
         # the prefill batch of the 2B shape
-        _ffn("ffn fwd, 16384 tokens", False, 16384, 2048, 8192, "silu"),
+        _ffn("ffn fwd 16384 tokens", False, 16384, 2048, 8192, "silu"),
         # ragged training step: a part-filled batch on the 0.5B shape
-        _ffn("ffn step, 1003 tokens", True, 1003, 1024, 4096, "gelu_tanh"),
+        _ffn("ffn step 1003 tokens", True, 1003, 1024, 4096, "gelu_tanh"),
         # the training batch of the 2B shape
-        _ffn("ffn step, 8192 tokens", True, 8192, 2048, 8192, "silu"),
+        _ffn("ffn step 8192 tokens", True, 8192, 2048, 8192, "silu"),
         # a few norm vectors and gates: many tensors, hardly any work
-        _adamw("adamw 32, 12 vectors", ",".join(["2048"] * 9 + ["1024", "1000", "1"]), 32, "f32",
+        _adamw("adamw 32 12 vectors", ",".join(["2048"] * 9 + ["1024", "1000", "1"]), 32, "f32",
                "f32", False),
         # a 2B layer: three FFN matrices and three vectors; bf16 weights, fp32 masters and gradients
-        _adamw("adamw 32, 2B layer", "%d,%d,%d,%d,%d,%d" % (M, M, M, V, V, V), 32, "bf16", "f32",
+        _adamw("adamw 32 2B layer", "%d,%d,%d,%d,%d,%d" % (M, M, M, V, V, V), 32, "bf16", "f32",
                True),
         # the same layer with 8-bit states, and bf16 gradients
-        _adamw("adamw 8, 2B layer", "%d,%d,%d,%d,%d,%d" % (M, M, M, V, V, V + 1), 8, "bf16", "bf16",
+        _adamw("adamw 8 2B layer", "%d,%d,%d,%d,%d,%d" % (M, M, M, V, V, V + 1), 8, "bf16", "bf16",
                True),
     ]
 
