@@ -1,11 +1,14 @@
 // abi.cu -- extern "C" entry points of libtwell.so: argument validation
 // (before any launch) and dispatch to the kernels.  The library never
 // allocates device memory and never synchronises the caller's stream.
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "tw_internal.h"
 
@@ -308,6 +311,76 @@ tw_status twell_ffn_small_batch(const void* x, const void* Wg_t, const void* Wu_
   if (ws_bytes < tw::decode_ws_bytes(T, d, F)) return TW_ERR_WORKSPACE;
   return from_cuda(tw::launch_decode_step(x, Wg_t, Wu_t, Wd, T, d, F, *g, g_dense_dump, y,
                                           y_dtype, ws, dev_status, stream));
+}
+
+// One array of an optimiser step, for the check that written arrays are apart.
+struct AdamwRange {
+  uintptr_t first, last;
+  bool written;
+};
+
+static tw_status check_adamw_tensor(const tw_adamw_tensor& t, std::vector<AdamwRange>* ranges) {
+  if (t.n < 0 || !dtype_ok(t.p_dtype) || !dtype_ok(t.g_dtype) ||
+      !(t.weight_decay >= 0.0 && std::isfinite(t.weight_decay)))
+    return TW_ERR_INVALID_ARG;
+  if (t.state_bits != 8 && t.state_bits != 32) return TW_ERR_UNSUPPORTED;
+  if (t.n > (int64_t(1) << 40)) return TW_ERR_UNSUPPORTED;
+  const bool small = t.state_bits == 8;
+  if (t.n == 0) return TW_OK;
+  if (!t.p || !t.g || !t.m || !t.v) return TW_ERR_INVALID_ARG;
+  if (t.master && t.p_dtype != TW_BF16) return TW_ERR_INVALID_ARG;
+  if (small != (t.m_scale != nullptr) || small != (t.v_scale != nullptr)) return TW_ERR_INVALID_ARG;
+  if ((t.m_values != nullptr) != (t.v_values != nullptr)) return TW_ERR_INVALID_ARG;
+  if (t.m_values && (!small || !dtype_ok(t.values_dtype))) return TW_ERR_INVALID_ARG;
+  const size_t n = (size_t)t.n, blocks = (n + TW_ADAMW_BLOCK - 1) / TW_ADAMW_BLOCK;
+  const size_t pb = t.p_dtype == TW_BF16 ? 2 : 4, gb = t.g_dtype == TW_BF16 ? 2 : 4;
+  const size_t sb = small ? 1 : 4, vb = t.values_dtype == TW_BF16 ? 2 : 4;
+  const struct { const void* at; size_t bytes; bool written; } arrays[] = {
+      {t.p, n * pb, true},           {t.master, n * 4, true},        {t.g, n * gb, false},
+      {t.m, n * sb, true},           {t.v, n * sb, true},            {t.m_scale, blocks * 4, true},
+      {t.v_scale, blocks * 4, true}, {t.m_values, n * vb, true},     {t.v_values, n * vb, true}};
+  for (const auto& a : arrays) {
+    if (!a.at) continue;
+    if (!aligned16(a.at)) return TW_ERR_ALIGNMENT;
+    const uintptr_t first = reinterpret_cast<uintptr_t>(a.at);
+    ranges->push_back({first, first + a.bytes, a.written});
+  }
+  return TW_OK;
+}
+
+tw_status adamw_step(const tw_adamw_tensor* tensors, int32_t count, const tw_adamw_args* args,
+                     cudaStream_t stream) {
+  if (count < 0 || (count > 0 && !tensors) || !args) return TW_ERR_INVALID_ARG;
+  const double scalars[] = {args->lr, args->beta1, args->beta2, args->eps};
+  for (double v : scalars)
+    if (!std::isfinite(v) || v < 0.0) return TW_ERR_INVALID_ARG;
+  if (args->beta1 >= 1.0 || args->beta2 >= 1.0 || (float)args->eps <= 0.f)
+    return TW_ERR_INVALID_ARG;
+  if (!args->step_dev && args->step < 1) return TW_ERR_INVALID_ARG;
+  const void* words[] = {args->lr_dev, args->step_dev, args->grad_scale};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return TW_ERR_ALIGNMENT;
+  // no exception may leave a C entry
+  try {
+    std::vector<AdamwRange> ranges;
+    ranges.reserve(9 * (size_t)count);
+    for (int32_t i = 0; i < count; ++i) {
+      tw_status st = check_adamw_tensor(tensors[i], &ranges);
+      if (st != TW_OK) return st;
+    }
+    std::sort(ranges.begin(), ranges.end(),
+              [](const AdamwRange& a, const AdamwRange& b) { return a.first < b.first; });
+    // sweep by start: the furthest end of the written and of all ranges so far
+    uintptr_t end_written = 0, end_any = 0;
+    for (const AdamwRange& r : ranges) {
+      if (r.first < (r.written ? end_any : end_written)) return TW_ERR_INVALID_ARG;
+      end_any = std::max(end_any, r.last);
+      if (r.written) end_written = std::max(end_written, r.last);
+    }
+  } catch (...) {
+    return TW_ERR_UNSUPPORTED;  // no host memory for the list's ranges
+  }
+  return from_cuda(tw::launch_adamw(tensors, count, *args, stream));
 }
 
 // Workspace of the dense training comparator: g, u, h (saved by the forward

@@ -28,7 +28,7 @@ EXPORTS = ["twell_gate_gemm", "twell_fused_updown_workspace_size", "twell_fused_
            "hybrid_ffn_forward",
            "hybrid_ffn_backward_workspace_size", "hybrid_ffn_backward", "dense_ffn_forward",
            "dense_ffn_train_workspace_size", "dense_ffn_train_saved_bytes",
-           "dense_ffn_train_forward", "dense_ffn_train_backward",
+           "dense_ffn_train_forward", "dense_ffn_train_backward", "adamw_step",
            "tw_test_withhold_next_gate_loads", "tw_measure_row_gather", "tw_measure_stream_read", "tw_status_string",
            "twell_version"]
 
@@ -56,6 +56,22 @@ class TwHybridC(ctypes.Structure):
                 ("row_slot", ctypes.c_void_p), ("backup_cap", ctypes.c_int32),
                 ("backup_rows", ctypes.c_void_p), ("backup_g", ctypes.c_void_p),
                 ("backup_u", ctypes.c_void_p), ("n_backup", ctypes.c_void_p)]
+
+
+class TwAdamwTensorC(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("p", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("m_values", ctypes.c_void_p), ("v_values", ctypes.c_void_p),
+                ("p_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int),
+                ("values_dtype", ctypes.c_int), ("state_bits", ctypes.c_int32),
+                ("weight_decay", ctypes.c_double)]
+
+
+class TwAdamwArgsC(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int32), ("lr_dev", ctypes.c_void_p),
+                ("step_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -100,6 +116,8 @@ def lib():
                                               vp, vp, vp]
         L.dense_ffn_train_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, ctypes.c_float,
                                                vp, ctypes.c_size_t, vp, vp, vp, vp, vp, vp]
+        L.adamw_step.argtypes = [ctypes.POINTER(TwAdamwTensorC), i32,
+                                 ctypes.POINTER(TwAdamwArgsC), vp]
         L.tw_test_withhold_next_gate_loads.argtypes = [ctypes.c_uint64]
         L.tw_test_withhold_next_gate_loads.restype = None
         L.tw_measure_row_gather.argtypes = [vp, i32, i32, ctypes.c_int64, ctypes.c_uint32, vp,
@@ -113,7 +131,7 @@ def lib():
         for name in ("twell_gate_gemm", "twell_fused_updown", "twell_ffn_small_batch",
                      "twell_to_hybrid",
                      "hybrid_ffn_forward", "hybrid_ffn_backward", "dense_ffn_forward",
-                     "dense_ffn_train_forward", "dense_ffn_train_backward"):
+                     "dense_ffn_train_forward", "dense_ffn_train_backward", "adamw_step"):
             getattr(L, name).restype = st
         _lib = L
     return _lib
@@ -148,6 +166,27 @@ def _stream(stream):
 def _check(fn, code):
     if code != 0:
         raise TwellError(fn, code)
+
+
+def _same_device(tensors):
+    """The one CUDA device of the tensors (None entries skipped)."""
+    found = {t.device for t in tensors if t is not None}
+    if len(found) != 1 or next(iter(found)).type != "cuda":
+        raise ValueError("tensors passed to libtwell must be on one CUDA device")
+    return found.pop()
+
+
+def _call_on(device, fn, stream, *args):
+    """lib().<fn>(*args, stream) with `device` current, on its current stream
+    unless one is given."""
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream and the tensors are on different devices")
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == device.index:
+        _check(fn, f(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, f(*args, _stream(stream)))
 
 
 class Twell:
@@ -335,6 +374,86 @@ def dense_train_saved(ws, T, F):
     """Views of the g, u, h [T][F] bf16 tensors the training forward saved in ws."""
     part = (T * F * 2 + 255) // 256 * 256
     return [ws[i * part:i * part + T * F * 2].view(torch.bfloat16).view(T, F) for i in range(3)]
+
+
+ADAMW_BLOCK = 256  # elements that share one scale of an 8-bit moment
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step, packed once for many steps.
+
+    ``tensors``: mappings with p, g (bf16 or fp32), m, v and optionally master
+    (fp32, for a bf16 p), weight_decay (default 0), and for 8-bit moments
+    (m int8, v uint8) m_scale and v_scale (fp32, ``adamw_blocks(n)`` long) and
+    m_values, v_values, which receive what the new codes stand for.  The
+    tensors stay referenced; a program that puts another storage behind one of
+    them builds a new list."""
+
+    def __init__(self, tensors):
+        tensors = [dict(t) for t in tensors]
+        self._c = (TwAdamwTensorC * max(len(tensors), 1))()
+        self.count = len(tensors)
+        self._keep = []
+        for c, t in zip(self._c, tensors):
+            self._pack(c, t)
+        self.device = _same_device([x for t, _ in self._keep for x in t]) if self._keep else None
+        self._args = TwAdamwArgsC()
+
+    def _pack(self, c, t):
+        names = ("p", "master", "g", "m", "v", "m_scale", "v_scale", "m_values", "v_values")
+        unknown = set(t) - set(names) - {"weight_decay"}
+        if unknown:
+            raise TypeError(f"unknown keys {sorted(unknown)}")
+        get = {k: t.get(k) for k in names}
+        for k in ("p", "g", "m", "v"):
+            if get[k] is None:
+                raise ValueError(f"{k} is missing")
+        n = get["p"].numel()
+        small = get["m"].dtype == torch.int8
+        want = {"master": torch.float32, "m": torch.int8 if small else torch.float32,
+                "v": torch.uint8 if small else torch.float32,
+                "m_scale": torch.float32, "v_scale": torch.float32}
+        given = {k: x for k, x in get.items() if x is not None}
+        for k, x in given.items():
+            if k in want and x.dtype != want[k]:
+                raise TypeError(f"{k} is {x.dtype}, not {want[k]}")
+            if x.numel() != (adamw_blocks(n) if k.endswith("_scale") else n):
+                raise ValueError(f"{k} has {x.numel()} elements for a parameter of {n}")
+        for k, x in given.items():
+            setattr(c, k, _ptr(x))
+        c.n = n
+        c.p_dtype, c.g_dtype = _dt(get["p"]), _dt(get["g"])
+        if get["m_values"] is not None:
+            c.values_dtype = _dt(get["m_values"])
+            if get["v_values"] is not None and get["v_values"].dtype != get["m_values"].dtype:
+                raise TypeError("m_values and v_values differ in dtype")
+        c.state_bits = 8 if small else 32
+        c.weight_decay = float(t.get("weight_decay", 0.0))
+        held = list(given.values())
+        # the storages too: an address in the list must not outlive its memory
+        self._keep.append((held, [x.untyped_storage() for x in held]))
+
+
+def adamw_blocks(n):
+    """Block scales of an 8-bit moment of n elements."""
+    return (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+
+
+def adamw_step(tensors: AdamWTensors, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, lr_dev=None,
+               step_dev=None, grad_scale=None, stream=None):
+    """One AdamW step over all tensors of the list, in one launch for up to 256
+    of them.  lr_dev (fp32), step_dev (int32) and grad_scale (fp32) are device
+    tensors of one element that a captured step reads at each replay."""
+    if tensors.count == 0:
+        return
+    for x, dtype in ((lr_dev, torch.float32), (step_dev, torch.int32),
+                     (grad_scale, torch.float32)):
+        if x is not None and (x.dtype != dtype or x.numel() != 1 or x.device != tensors.device):
+            raise ValueError(f"device scalars are one {dtype} on {tensors.device}")
+    a = tensors._args
+    a.lr, a.beta1, a.beta2, a.eps, a.step = lr, beta1, beta2, eps, step
+    a.lr_dev, a.step_dev, a.grad_scale = _ptr(lr_dev), _ptr(step_dev), _ptr(grad_scale)
+    _call_on(tensors.device, "adamw_step", stream, tensors._c, tensors.count, ctypes.byref(a))
 
 
 def status_bits(dev_status) -> list:

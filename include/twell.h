@@ -317,6 +317,80 @@ TW_API tw_status dense_ffn_train_backward(const void* x, const void* dy, const v
                                           int32_t* dev_status, cudaStream_t stream);
 
 /*
+ * Multi-tensor AdamW step, for the weights the training calls give gradients
+ * of.  One tensor of a step, n elements, contiguous:
+ *   p        the parameter (p_dtype), updated; with a master copy it receives
+ *            the rounded master
+ *   master   fp32 copy the update runs on, or NULL (bf16 p only; without one a
+ *            bf16 p is widened, updated and rounded, and updates under half its
+ *            spacing are lost)
+ *   g        the gradient (g_dtype), read only
+ *   m, v     the two moments, updated.  state_bits 32: fp32.  state_bits 8:
+ *            one code per element and one fp32 scale per block of
+ *            TW_ADAMW_BLOCK consecutive elements (m_scale, v_scale, of
+ *            ceil(n / TW_ADAMW_BLOCK) floats):
+ *              m int8   c in [-127, 127]  m = m_scale * c * |c|
+ *              v uint8  c in [0, 255]     v = (v_scale * c * c)^2
+ *            The scale puts the block's largest magnitude on the largest code;
+ *            others go to the nearest code in the square root of the ratio,
+ *            and a v that is not zero keeps a code that is not zero.  A NaN or
+ *            infinite moment makes its whole block NaN; a block of m whose
+ *            largest magnitude is below 2^-127 is held as zero.  All-zero
+ *            codes and scales are the states of a first step.
+ *   m_values, v_values
+ *            state_bits 8 only, both or neither: receive what the new codes
+ *            stand for (values_dtype) -- an aid for inspection and tests; NULL
+ *            for speed
+ *   weight_decay  decoupled decay of this tensor (0 for norms and gates)
+ */
+#define TW_ADAMW_BLOCK 256
+typedef struct {
+  int64_t n;
+  void* p;
+  float* master;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* m_values;
+  void* v_values;
+  tw_dtype p_dtype, g_dtype, values_dtype;
+  int32_t state_bits;
+  double weight_decay;
+} tw_adamw_tensor;
+
+/*
+ * Scalars of a step, shared by its tensors.  step counts from 1.  The three
+ * device words may be NULL; they let a captured step change between replays:
+ * lr_dev (one float) takes the place of lr, step_dev (one int32, values below
+ * 1 count as 1) that of step, and every gradient is multiplied by *grad_scale
+ * (one float: a clipping factor, or the inverse of a loss scale) as it is read.
+ */
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int32_t step;
+  const float* lr_dev;
+  const int32_t* step_dev;
+  const float* grad_scale;
+} tw_adamw_args;
+
+/*
+ * For every element of every tensor, in fp32 (the bias corrections in fp64):
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
+ *   p = p (1 - lr wd) - lr/(1 - beta1^step) * m / (sqrt(v/(1 - beta2^step)) + eps).
+ * The parameter moves by the moments as computed; only what is kept of them is
+ * rounded to 8 bits.  The descriptors travel in the launch, up to 36 tensors
+ * in a small one and 256 in a large one; longer lists take several launches.
+ * `tensors` is read during the call only.  0 <= beta < 1, eps > 0.  Tensors
+ * with n == 0 are skipped and their pointers may be NULL.  No written array may
+ * overlap another array of the list (TW_ERR_INVALID_ARG): the same parameter
+ * twice in one step has no defined order.
+ */
+TW_API tw_status adamw_step(const tw_adamw_tensor* tensors, int32_t count,
+                            const tw_adamw_args* args, cudaStream_t stream);
+
+/*
  * Test aid for the bounded pipeline waits; not needed in normal use.  The
  * next twell_gate_gemm call that runs the tile GEMM (T > 64, or any T when
  * W != 128) withholds its TMA loads and bounds its waits by wait_limit_ns:
