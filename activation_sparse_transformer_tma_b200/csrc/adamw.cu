@@ -18,6 +18,13 @@
 // eps.  The moments are rounded to nearest once a step; the update itself uses
 // them unrounded.
 //
+// One block a warp and five CTAs of eight warps on an SM: more blocks a warp (16,
+// 32 or 64 a CTA) were 2 to 20% slower, since a warp's loads do not overlap its
+// own arithmetic, and forcing six CTAs on an SM spilled registers.  Measured on the
+// three 8192 x 2048 matrices of a 2B layer: fp32 moments, fp32 masters and
+// gradients, bf16 weights (30 bytes an element) 225 us, 6.7 TB/s; 8-bit moments, bf16
+// gradients, with the values written (20 bytes) 185 us, 5.4 TB/s.
+//
 // The tensors' descriptors travel as kernel parameters: nothing has to stay
 // alive after the call and a captured step replays with them.
 #include "pdl.cuh"
@@ -32,7 +39,8 @@ namespace {
 constexpr int kBlock = TW_ADAMW_BLOCK;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlocksPerCta = 32;  // 8192 elements: four blocks a warp
+constexpr int kBlocksPerCta = kWarps;  // one block a warp
+constexpr int kCtasPerSm = 5;          // 48 registers a thread
 static_assert(kBlock == 256, "a warp holds a block as two halves of 4 elements a lane");
 
 struct Tensor {
@@ -47,6 +55,7 @@ struct Tensor {
   void* m_values;
   void* v_values;
   double decay;
+  float keep;  // 1 - lr * decay, unless lr_dev is given
   uint32_t p_bf16 : 1, g_bf16 : 1, values_bf16 : 1, small : 1;
 };
 
@@ -54,6 +63,8 @@ struct Scalars {
   double lr, beta1, beta2;
   double bias1, bias2;  // 1 - beta^step, unless step_dev is given
   float eps, b1, c1, b2, c2;
+  float size, rsqrt_bias2;  // lr / bias1 and 1 / sqrt(bias2) without device scalars
+  bool dynamic;             // any device scalar
   const float* lr_dev;
   const int32_t* step_dev;
   const float* grad_scale;
@@ -126,31 +137,37 @@ TW_DEV float sqrt_approx(float x) {
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// What codes stand for: m, and sqrt(v).
-TW_DEV float m_of(int c, float scale) { return (float)(c * (c < 0 ? -c : c)) * scale; }
-TW_DEV float root_of(int c, float scale) { return (float)(c * c) * scale; }
+
+// Codes and floats without conversion instructions, which run at a quarter of
+// the rate: a byte in the low mantissa bits of 2^23 is that integer above 2^23,
+// and adding 1.5 * 2^23 rounds a small float to the nearest integer, in two's
+// complement in the low bits.
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+TW_DEV float byte_above_2_23(uint32_t word, int k) {
+  return __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440u + k));
+}
+TW_DEV uint32_t pack_bytes(const float (&a)[4]) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a[0]), __float_as_uint(a[1]), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(a[2]), __float_as_uint(a[3]), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
 
 struct Step {
   float gscale, b1, c1, b2, c2, rsqrt_bias2, eps, size, keep;
 };
 
-// Moments and parameter of one element.
-TW_DEV void update(const Step& st, float g, float& m, float& v, float& p) {
-  g *= st.gscale;
-  m = fmaf(st.b1, m, st.c1 * g);
-  v = fmaf(st.b2, v, st.c2 * g * g);
-  p = fmaf(p, st.keep, -st.size * __fdiv_rn(m, fmaf(sqrtf(v), st.rsqrt_bias2, st.eps)));
-}
-
-// One block of 256 elements by one warp; `full`: none of them past n.
-template <bool SMALL>
+// One block of 256 elements by one warp (FULL: all of them exist).  With 8-bit moments the square roots
+// and the division are the approximate instructions (2 ulp, against codes
+// that are off by up to 0.8%): the IEEE forms' extra instructions, not memory,
+// bounded that form.
+template <bool SMALL, bool FULL>
 TW_DEV void step_block(const Tensor& t, const Step& st, int64_t block, int lane) {
   const int64_t at[2] = {block * kBlock + lane * 4, block * kBlock + 128 + lane * 4};
   int valid[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t left = t.n - at[h];
-    valid[h] = left >= 4 ? 4 : left > 0 ? (int)left : 0;
+    valid[h] = FULL || left >= 4 ? 4 : left > 0 ? (int)left : 0;
   }
   const void* from = t.master ? static_cast<const void*>(t.master) : t.p;
   const bool from_bf16 = t.p_bf16 && !t.master;
@@ -176,22 +193,31 @@ TW_DEV void step_block(const Tensor& t, const Step& st, int64_t block, int lane)
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        m[h][k] = m_of((int8_t)(mc[h] >> (8 * k)), ms);
-        const float root = root_of((uint8_t)(vc[h] >> (8 * k)), vs);
+        const float c = byte_above_2_23(mc[h] ^ 0x80808080u, k) - 8388736.f;  // 2^23 + 128
+        m[h][k] = c * fabsf(c) * ms;
+        const float b = byte_above_2_23(vc[h], k) - 8388608.f;
+        const float root = b * b * vs;
         v[h][k] = root * root;
       }
   }
+  float root[2][4];
   uint32_t mtop = 0, vtop = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      update(st, g[h][k], m[h][k], v[h][k], p[h][k]);
+      const float gs = g[h][k] * st.gscale;
+      const float mn = m[h][k] = fmaf(st.b1, m[h][k], st.c1 * gs);
+      const float vn = v[h][k] = fmaf(st.b2, v[h][k], st.c2 * gs * gs);
+      const float r = root[h][k] = SMALL ? sqrt_approx(vn) : sqrtf(vn);
+      const float den = fmaf(r, st.rsqrt_bias2, st.eps);
+      const float q = SMALL ? __fdividef(mn, den) : __fdiv_rn(mn, den);
+      p[h][k] = fmaf(p[h][k], st.keep, -st.size * q);
       // elements past n take no part in the block's maximum, whatever a
-      // block scale of NaN or infinity made of them
+      // block scale of NaN made of them
       if (SMALL && k < valid[h]) {
-        mtop = max(mtop, __float_as_uint(m[h][k]) & 0x7FFFFFFFu);
-        vtop = max(vtop, __float_as_uint(v[h][k]));
+        mtop = max(mtop, __float_as_uint(mn) & 0x7FFFFFFFu);
+        vtop = max(vtop, __float_as_uint(r));
       }
     }
 #pragma unroll
@@ -205,7 +231,7 @@ TW_DEV void step_block(const Tensor& t, const Step& st, int64_t block, int lane)
   }
   if (!SMALL) return;
   const float mmax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mtop));
-  const float vmax = sqrtf(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, vtop)));
+  const float vmax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, vtop));
   // below 2^-127 the reciprocal is infinite: such a block of m is held as zero
   const float minv = mmax < 5.9e-39f ? 0.f : 1.f / mmax;
   const float vinv = vmax == 0.f ? 0.f : 1.f / vmax;
@@ -219,33 +245,34 @@ TW_DEV void step_block(const Tensor& t, const Step& st, int64_t block, int lane)
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t mw = 0, vw = 0;
-    float mval[4], vval[4];
+    float mw[4], vw[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int a = __float2int_rn(127.f * sqrt_approx(fabsf(m[h][k]) * minv));
-      const int c = m[h][k] < 0.f ? -a : a;
-      int b = __float2int_rn(255.f * sqrt_approx(sqrt_approx(v[h][k]) * vinv));
-      if (b == 0 && v[h][k] > 0.f) b = 1;
-      mw |= (uint32_t)(c & 255) << (8 * k);
-      vw |= (uint32_t)(b & 255) << (8 * k);
-      mval[k] = m_of(c, ms);
-      const float root = root_of(b, vs);
-      vval[k] = root * root;
+      mw[k] = copysignf(127.f * sqrt_approx(fabsf(m[h][k]) * minv), m[h][k]) + kMagic;
+      // at least code 1 where v is not zero: one position below it rounds up to it
+      const float pos = 255.f * sqrt_approx(root[h][k] * vinv);
+      vw[k] = (root[h][k] > 0.f ? fmaxf(pos, 1.f) : pos) + kMagic;
     }
-    store_codes(t.m, at[h], valid[h], mw);
-    store_codes(t.v, at[h], valid[h], vw);
+    store_codes(t.m, at[h], valid[h], pack_bytes(mw));
+    store_codes(t.v, at[h], valid[h], pack_bytes(vw));
     if (t.m_values) {
-      store4(t.m_values, t.values_bf16, at[h], valid[h], mval);
-      store4(t.v_values, t.values_bf16, at[h], valid[h], vval);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float c = mw[k] - kMagic, b = vw[k] - kMagic;
+        mw[k] = c * fabsf(c) * ms;
+        const float r = b * b * vs;
+        vw[k] = r * r;
+      }
+      store4(t.m_values, t.values_bf16, at[h], valid[h], mw);
+      store4(t.v_values, t.values_bf16, at[h], valid[h], vw);
     }
   }
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     adamw_kernel(const __grid_constant__ Batch<CAP> b) {
-  __shared__ Step shared_step;
+  __shared__ Step dynamic;
   const int cta = blockIdx.x;
   int lo = 0, hi = b.count - 1;  // the last tensor whose first CTA is not past this one
   while (lo < hi) {
@@ -256,52 +283,63 @@ __global__ void __launch_bounds__(kThreads)
   const Tensor& t = b.t[lo];
   pdl_wait();
   pdl_launch_next();
-  if (threadIdx.x == 0) {
-    const Scalars& s = b.s;
-    double bias1 = s.bias1, bias2 = s.bias2;
-    if (s.step_dev) {
-      // beta^step by squaring, in fp64: 1 - beta^step loses digits in fp32
-      const int32_t at = *s.step_dev;
-      double p1 = 1.0, p2 = 1.0, q1 = s.beta1, q2 = s.beta2;
-      for (int32_t e = at < 1 ? 1 : at; e > 0; e >>= 1) {
-        if (e & 1) {
-          p1 *= q1;
-          p2 *= q2;
+  const Scalars& s = b.s;
+  Step st;
+  st.gscale = 1.f;
+  st.b1 = s.b1;
+  st.c1 = s.c1;
+  st.b2 = s.b2;
+  st.c2 = s.c2;
+  st.eps = s.eps;
+  st.rsqrt_bias2 = s.rsqrt_bias2;
+  st.size = s.size;
+  st.keep = t.keep;
+  if (s.dynamic) {
+    if (threadIdx.x == 0) {
+      double bias1 = s.bias1, bias2 = s.bias2;
+      if (s.step_dev) {
+        // beta^step by squaring, in fp64: 1 - beta^step loses digits in fp32
+        const int32_t at = *s.step_dev;
+        double p1 = 1.0, p2 = 1.0, q1 = s.beta1, q2 = s.beta2;
+        for (int32_t e = at < 1 ? 1 : at; e > 0; e >>= 1) {
+          if (e & 1) {
+            p1 *= q1;
+            p2 *= q2;
+          }
+          q1 *= q1;
+          q2 *= q2;
         }
-        q1 *= q1;
-        q2 *= q2;
+        bias1 = 1.0 - p1;
+        bias2 = 1.0 - p2;
       }
-      bias1 = 1.0 - p1;
-      bias2 = 1.0 - p2;
+      const double lr = s.lr_dev ? (double)*s.lr_dev : s.lr;
+      dynamic.gscale = s.grad_scale ? *s.grad_scale : 1.f;
+      dynamic.rsqrt_bias2 = (float)(1.0 / sqrt(bias2));
+      dynamic.size = (float)(lr / bias1);
+      dynamic.keep = (float)(1.0 - lr * t.decay);
     }
-    const double lr = s.lr_dev ? (double)*s.lr_dev : s.lr;
-    Step st;
-    st.gscale = s.grad_scale ? *s.grad_scale : 1.f;
-    st.b1 = s.b1;
-    st.c1 = s.c1;
-    st.b2 = s.b2;
-    st.c2 = s.c2;
-    st.rsqrt_bias2 = (float)(1.0 / sqrt(bias2));
-    st.eps = s.eps;
-    st.size = (float)(lr / bias1);
-    st.keep = (float)(1.0 - lr * t.decay);
-    shared_step = st;
+    __syncthreads();
+    st.gscale = dynamic.gscale;
+    st.rsqrt_bias2 = dynamic.rsqrt_bias2;
+    st.size = dynamic.size;
+    st.keep = dynamic.keep;
   }
-  __syncthreads();
-  const Step st = shared_step;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t blocks = (t.n + kBlock - 1) / kBlock;
-  const int64_t first = (int64_t)(cta - b.first_cta[lo]) * kBlocksPerCta;
-  const int64_t last = first + kBlocksPerCta < blocks ? first + kBlocksPerCta : blocks;
-  for (int64_t i = first + warp; i < last; i += kWarps) {
-    if (t.small) step_block<true>(t, st, i, lane);
-    else step_block<false>(t, st, i, lane);
+  const int64_t i = (int64_t)(cta - b.first_cta[lo]) * kBlocksPerCta + warp;
+  if (i * kBlock >= t.n) return;
+  const bool full = t.n - i * kBlock >= kBlock;
+  if (t.small) {
+    if (full) step_block<true, true>(t, st, i, lane);
+    else step_block<true, false>(t, st, i, lane);
+  } else {
+    if (full) step_block<false, true>(t, st, i, lane);
+    else step_block<false, false>(t, st, i, lane);
   }
 }
 
 // Kernel parameters end at 32,764 bytes; the small form keeps the usual step
 // of one layer within the 4 KB that every launch copies cheaply.
-constexpr int kFew = 36, kMany = 256;
+constexpr int kFew = 32, kMany = 256;
 static_assert(sizeof(Batch<kFew>) <= 4096 && sizeof(Batch<kMany>) <= 32764, "parameter space");
 
 // Takes tensors from `at` on, as many as fit; returns the next one to take.
@@ -331,6 +369,7 @@ cudaError_t launch_some(const tw_adamw_tensor* tensors, int count, int* at, cons
     d.m_values = t.m_values;
     d.v_values = t.v_values;
     d.decay = t.weight_decay;
+    d.keep = (float)(1.0 - s.lr * t.weight_decay);
     d.p_bf16 = t.p_dtype == TW_BF16;
     d.g_bf16 = t.g_dtype == TW_BF16;
     d.values_bf16 = t.values_dtype == TW_BF16;
@@ -359,6 +398,9 @@ cudaError_t launch_adamw(const tw_adamw_tensor* tensors, int count, const tw_ada
   s.c1 = (float)(1.0 - a.beta1);
   s.b2 = (float)a.beta2;
   s.c2 = (float)(1.0 - a.beta2);
+  s.size = (float)(s.lr / s.bias1);
+  s.rsqrt_bias2 = (float)(1.0 / std::sqrt(s.bias2));
+  s.dynamic = a.lr_dev || a.step_dev || a.grad_scale;
   s.lr_dev = a.lr_dev;
   s.step_dev = a.step_dev;
   s.grad_scale = a.grad_scale;

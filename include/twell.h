@@ -380,7 +380,7 @@ typedef struct {
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
  *   p = p (1 - lr wd) - lr/(1 - beta1^step) * m / (sqrt(v/(1 - beta2^step)) + eps).
  * The parameter moves by the moments as computed; only what is kept of them is
- * rounded to 8 bits.  The descriptors travel in the launch, up to 36 tensors
+ * rounded to 8 bits.  The descriptors travel in the launch, up to 32 tensors
  * in a small one and 256 in a large one; longer lists take several launches.
  * `tensors` is read during the call only.  0 <= beta < 1, eps > 0.  Tensors
  * with n == 0 are skipped and their pointers may be NULL.  No written array may
