@@ -313,6 +313,79 @@ tw_status twell_ffn_small_batch(const void* x, const void* Wg_t, const void* Wu_
                                           y_dtype, ws, dev_status, stream));
 }
 
+static tw_status check_norm_block(const tw_norm_block* b, bool has_y) {
+  if (!b) return TW_ERR_INVALID_ARG;
+  if (b->T < 0 || b->d <= 0 || !dtype_ok(b->y_dtype) || !dtype_ok(b->r_dtype) ||
+      !dtype_ok(b->n_dtype) || !dtype_ok(b->w_dtype))
+    return TW_ERR_INVALID_ARG;
+  if (!(b->eps >= 0.f) || !std::isfinite(b->eps) || !std::isfinite(b->res_scale) ||
+      !std::isfinite(b->block_scale))
+    return TW_ERR_INVALID_ARG;
+  if (b->d % 8 != 0 || b->d > tw::kNormMaxD) return TW_ERR_UNSUPPORTED;
+  if (b->gate && b->gate_group < 1) return TW_ERR_INVALID_ARG;
+  if (!has_y && (b->w_post || b->gate || !b->w_pre)) return TW_ERR_INVALID_ARG;
+  if (!aligned16(b->w_post) || !aligned16(b->gate) || !aligned16(b->w_pre))
+    return TW_ERR_ALIGNMENT;
+  return TW_OK;
+}
+
+tw_status norm_residual_forward(const tw_norm_block* b, const void* y, const void* r, void* r_out,
+                                void* n_out, float* rstd_post, float* rstd_pre,
+                                cudaStream_t stream) {
+  // with no tokens the arrays sized by T may all be NULL, y among them
+  const bool any = b && b->T > 0;
+  tw_status st = check_norm_block(b, !any || y);
+  if (st != TW_OK) return st;
+  const void* ptrs[] = {y, r, r_out, n_out, rstd_post, rstd_pre};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return TW_ERR_ALIGNMENT;
+  if (!any) return TW_OK;
+  if (!r || (y != nullptr) != (r_out != nullptr)) return TW_ERR_INVALID_ARG;
+  if ((b->w_pre != nullptr) != (n_out != nullptr) || (rstd_pre && !b->w_pre) ||
+      (rstd_post && !b->w_post))
+    return TW_ERR_INVALID_ARG;
+  return from_cuda(
+      tw::launch_norm_forward(*b, y, r, r_out, n_out, rstd_post, rstd_pre, stream));
+}
+
+size_t norm_residual_backward_workspace_size(int32_t T, int32_t d, int32_t gate_group) {
+  if (T < 0 || d <= 0 || gate_group < 0) return 0;
+  return tw::norm_backward_ws_bytes(T, d, gate_group);
+}
+
+tw_status norm_residual_backward(const tw_norm_block* b, const void* dn, const void* dr_out,
+                                 const void* y, const void* r_out, const float* rstd_post,
+                                 const float* rstd_pre, void* dy, void* dr, float* dw_post,
+                                 float* dgate, float* dw_pre, void* ws, size_t ws_bytes,
+                                 cudaStream_t stream) {
+  const bool any = b && b->T > 0;
+  tw_status st = check_norm_block(b, !any || y);
+  if (st != TW_OK) return st;
+  const void* ptrs[] = {dn, dr_out, y, r_out, rstd_post, rstd_pre, dy, dr, dw_post, dgate, dw_pre,
+                        ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return TW_ERR_ALIGNMENT;
+  if ((b->w_pre != nullptr) != (dw_pre != nullptr) || (b->w_post != nullptr) != (dw_post != nullptr))
+    return TW_ERR_INVALID_ARG;
+  if (!any) {  // no tokens: zero weight gradients, and no gate rows
+    const size_t bytes = sizeof(float) * (size_t)b->d;
+    cudaError_t e = dw_pre ? cudaMemsetAsync(dw_pre, 0, bytes, stream) : cudaSuccess;
+    if (e == cudaSuccess && dw_post) e = cudaMemsetAsync(dw_post, 0, bytes, stream);
+    return from_cuda(e);
+  }
+  if (!dr || (!dn && !dr_out) || (b->w_pre != nullptr) != (dn != nullptr)) return TW_ERR_INVALID_ARG;
+  if ((y != nullptr) != (dy != nullptr) || (b->gate != nullptr) != (dgate != nullptr))
+    return TW_ERR_INVALID_ARG;
+  if ((b->w_pre != nullptr) != (rstd_pre != nullptr) ||
+      (b->w_post != nullptr) != (rstd_post != nullptr) || (b->w_pre && !r_out))
+    return TW_ERR_INVALID_ARG;
+  if (!ws) return TW_ERR_INVALID_ARG;
+  if (ws_bytes < tw::norm_backward_ws_bytes(b->T, b->d, b->gate ? b->gate_group : 0))
+    return TW_ERR_WORKSPACE;
+  return from_cuda(tw::launch_norm_backward(*b, dn, dr_out, y, r_out, rstd_post, rstd_pre, dy, dr,
+                                            dw_post, dgate, dw_pre, ws, stream));
+}
+
 // One array of an optimiser step, for the check that written arrays are apart.
 struct AdamwRange {
   uintptr_t first, last;

@@ -131,6 +131,17 @@ cudaError_t launch_hybrid_backward(const void* x, const void* dy, const tw_hybri
                                    float* dWu_t, float* dWd, void* ws, size_t ws_bytes,
                                    int32_t* status, cudaStream_t stream);
 
+// Norms around a block (norm_residual.cu).  Arguments validated by the caller.
+constexpr int kNormMaxD = 8192;
+cudaError_t launch_norm_forward(const tw_norm_block& b, const void* y, const void* r, void* r_out,
+                                void* n_out, float* rstd_post, float* rstd_pre,
+                                cudaStream_t stream);
+size_t norm_backward_ws_bytes(int T, int d, int gate_group);
+cudaError_t launch_norm_backward(const tw_norm_block& b, const void* dn, const void* dr_out,
+                                 const void* y, const void* r_out, const float* rstd_post,
+                                 const float* rstd_pre, void* dy, void* dr, float* dw_post,
+                                 float* dgate, float* dw_pre, void* ws, cudaStream_t stream);
+
 // Multi-tensor AdamW (adamw.cu).  Arguments validated by the caller.
 cudaError_t launch_adamw(const tw_adamw_tensor* tensors, int count, const tw_adamw_args& args,
                          cudaStream_t stream);

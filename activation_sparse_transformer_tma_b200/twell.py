@@ -28,7 +28,9 @@ EXPORTS = ["twell_gate_gemm", "twell_fused_updown_workspace_size", "twell_fused_
            "hybrid_ffn_forward",
            "hybrid_ffn_backward_workspace_size", "hybrid_ffn_backward", "dense_ffn_forward",
            "dense_ffn_train_workspace_size", "dense_ffn_train_saved_bytes",
-           "dense_ffn_train_forward", "dense_ffn_train_backward", "adamw_step",
+           "dense_ffn_train_forward", "dense_ffn_train_backward",
+           "norm_residual_forward", "norm_residual_backward_workspace_size",
+           "norm_residual_backward", "adamw_step",
            "tw_test_withhold_next_gate_loads", "tw_measure_row_gather", "tw_measure_stream_read", "tw_status_string",
            "twell_version"]
 
@@ -56,6 +58,15 @@ class TwHybridC(ctypes.Structure):
                 ("row_slot", ctypes.c_void_p), ("backup_cap", ctypes.c_int32),
                 ("backup_rows", ctypes.c_void_p), ("backup_g", ctypes.c_void_p),
                 ("backup_u", ctypes.c_void_p), ("n_backup", ctypes.c_void_p)]
+
+
+class TwNormBlockC(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("gate_group", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int), ("r_dtype", ctypes.c_int), ("n_dtype", ctypes.c_int),
+                ("w_dtype", ctypes.c_int), ("res_scale", ctypes.c_float),
+                ("block_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p)]
 
 
 class TwAdamwTensorC(ctypes.Structure):
@@ -116,6 +127,12 @@ def lib():
                                               vp, vp, vp]
         L.dense_ffn_train_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, ctypes.c_float,
                                                vp, ctypes.c_size_t, vp, vp, vp, vp, vp, vp]
+        PN = ctypes.POINTER(TwNormBlockC)
+        L.norm_residual_forward.argtypes = [PN, vp, vp, vp, vp, vp, vp, vp]
+        L.norm_residual_backward_workspace_size.argtypes = [i32, i32, i32]
+        L.norm_residual_backward_workspace_size.restype = ctypes.c_size_t
+        L.norm_residual_backward.argtypes = [PN, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                             ctypes.c_size_t, vp]
         L.adamw_step.argtypes = [ctypes.POINTER(TwAdamwTensorC), i32,
                                  ctypes.POINTER(TwAdamwArgsC), vp]
         L.tw_test_withhold_next_gate_loads.argtypes = [ctypes.c_uint64]
@@ -131,13 +148,17 @@ def lib():
         for name in ("twell_gate_gemm", "twell_fused_updown", "twell_ffn_small_batch",
                      "twell_to_hybrid",
                      "hybrid_ffn_forward", "hybrid_ffn_backward", "dense_ffn_forward",
-                     "dense_ffn_train_forward", "dense_ffn_train_backward", "adamw_step"):
+                     "dense_ffn_train_forward", "dense_ffn_train_backward",
+                     "norm_residual_forward", "norm_residual_backward", "adamw_step"):
             getattr(L, name).restype = st
         _lib = L
     return _lib
 
 
 # ------------------------------------------------------------------ helpers --
+_DTYPE_CODES = {torch.bfloat16: TW_BF16, torch.float32: TW_F32}
+
+
 def _dt(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return TW_BF16
@@ -374,6 +395,91 @@ def dense_train_saved(ws, T, F):
     """Views of the g, u, h [T][F] bf16 tensors the training forward saved in ws."""
     part = (T * F * 2 + 255) // 256 * 256
     return [ws[i * part:i * part + T * F * 2].view(torch.bfloat16).view(T, F) for i in range(3)]
+
+
+def _norm_block(like, y, n, w_post, gate, w_pre, r_dtype, gate_group, res_scale, block_scale, eps):
+    """The shared descriptor of a norm call; `like` is a [T, d] tensor of it."""
+    T, d = like.shape
+    w_dtype = None
+    for w, rows in ((w_post, 1), (gate, -(-T // gate_group) if gate_group > 0 else 0), (w_pre, 1)):
+        if w is None:
+            continue
+        if w.numel() != rows * d:
+            raise ValueError(f"a weight of {w.numel()} elements for {rows} rows of {d}")
+        if w_dtype is not None and w.dtype != w_dtype:
+            raise TypeError("w_post, gate and w_pre differ in dtype")
+        w_dtype = w.dtype
+    codes = _DTYPE_CODES
+    try:
+        return TwNormBlockC(T, d, gate_group, TW_F32 if y is None else codes[y.dtype],
+                            codes[r_dtype], TW_F32 if n is None else codes[n.dtype],
+                            TW_F32 if w_dtype is None else codes[w_dtype], res_scale, block_scale,
+                            eps, _ptr(w_post), _ptr(gate), _ptr(w_pre))
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e.args[0]}") from None
+
+
+def _same_shape(like, *tensors):
+    for t in tensors:
+        if t is not None and t.shape != like.shape:
+            raise ValueError(f"shape {tuple(t.shape)} beside {tuple(like.shape)}")
+
+
+def _floats(n, *tensors):
+    for t in tensors:
+        if t is not None and (t.dtype != torch.float32 or t.numel() != n):
+            raise ValueError(f"{n} fp32 elements expected, got {t.numel()} of {t.dtype}")
+
+
+def norm_residual_forward(y, r, w_post, gate, w_pre, r_out, n_out, *, gate_group=0, res_scale=1.0,
+                          block_scale=1.0, eps=1e-6, rstd_post=None, rstd_pre=None, stream=None):
+    """r_out = res_scale r + block_scale gate norm(y) w_post and n_out = norm(r_out) w_pre, per
+    token of [T, d] tensors.  w_post, w_pre [d], gate [ceil(T / gate_group), d]; any of them may
+    be None, and y and r_out for the first norm of a network.  rstd_post, rstd_pre [T] fp32 keep
+    what norm_residual_backward needs."""
+    device = _same_device((y, r, w_post, gate, w_pre, r_out, n_out, rstd_post, rstd_pre))
+    _same_shape(r, y, r_out, n_out)
+    if r_out is not None and r_out.dtype != r.dtype:
+        raise TypeError("r and r_out differ in dtype")
+    _floats(r.shape[0], rstd_post, rstd_pre)
+    b = _norm_block(r, y, n_out, w_post, gate, w_pre, r.dtype, gate_group, res_scale, block_scale,
+                    eps)
+    _call_on(device, "norm_residual_forward", stream, ctypes.byref(b), _ptr(y), _ptr(r),
+             _ptr(r_out), _ptr(n_out), _ptr(rstd_post), _ptr(rstd_pre))
+
+
+def norm_residual_backward_workspace_size(T, d, gate_group=0):
+    return int(lib().norm_residual_backward_workspace_size(T, d, gate_group))
+
+
+def norm_residual_backward_workspace(T, d, gate_group=0, device="cuda"):
+    """A caller-owned workspace tensor for norm_residual_backward."""
+    with torch.cuda.device(device):
+        size = norm_residual_backward_workspace_size(T, d, gate_group)
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def norm_residual_backward(dn, dr_out, y, r_out, w_post, gate, w_pre, rstd_post, rstd_pre, dy, dr,
+                           dw_post, dgate, dw_pre, ws, *, gate_group=0, res_scale=1.0,
+                           block_scale=1.0, stream=None):
+    """Gradients of norm_residual_forward: dy, dr [T, d], dw_post, dw_pre [d] and dgate like gate
+    (fp32), from dn and dr_out, the gradients of n_out and r_out (either may be None; dn is None
+    exactly when w_pre is)."""
+    device = _same_device((dn, dr_out, y, r_out, w_post, gate, w_pre, rstd_post, rstd_pre, dy, dr,
+                           dw_post, dgate, dw_pre, ws))
+    _same_shape(dr, dn, dr_out, y, r_out, dy)
+    for a, b in ((dr_out, dr), (r_out, dr), (dy, y)):
+        if a is not None and b is not None and a.dtype != b.dtype:
+            raise TypeError("a gradient differs in dtype from its tensor")
+    _floats(dr.shape[0], rstd_post, rstd_pre)
+    _floats(dr.shape[1], dw_post, dw_pre)
+    if dgate is not None:
+        _floats(0 if gate is None else gate.numel(), dgate)
+    b = _norm_block(dr, y, dn, w_post, gate, w_pre, dr.dtype, gate_group, res_scale, block_scale,
+                    0.0)
+    _call_on(device, "norm_residual_backward", stream, ctypes.byref(b), _ptr(dn), _ptr(dr_out),
+             _ptr(y), _ptr(r_out), _ptr(rstd_post), _ptr(rstd_pre), _ptr(dy), _ptr(dr),
+             _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), _ptr(ws), ws.numel() * ws.element_size())
 
 
 ADAMW_BLOCK = 256  # elements that share one scale of an 8-bit moment

@@ -317,6 +317,68 @@ TW_API tw_status dense_ffn_train_backward(const void* x, const void* dy, const v
                                           int32_t* dev_status, cudaStream_t stream);
 
 /*
+ * The norms before and after a block (for instance the FFN), fused with the
+ * block's gate, its residual scale and the residual sum.  For token t, gate row
+ * q = t / gate_group and RMS norms without a mean:
+ *   o  = y * rstd_post * w_post     rstd_post = 1/sqrt(mean(y^2) + eps)
+ *        (o = y without w_post)
+ *   r' = res_scale * r + block_scale * gate[q] * o       (gate 1 without one)
+ *   n  = r' * rstd_pre * w_pre      rstd_pre = 1/sqrt(mean(r'^2) + eps)
+ * r' is the residual stream behind the block, n the next block's input.  r' is
+ * rounded once to r_dtype; n is computed from the unrounded r'.
+ *   w_post, w_pre  [d], gate [ceil(T / gate_group)][d], all w_dtype; each may
+ *             be NULL.  gate_group >= 1 with a gate (T or more: one row for all
+ *             tokens, 1: a row per token), ignored without one.
+ *   without w_pre there is no n: n_out and rstd_pre are NULL;
+ *   without y there is no block (the first norm of a network): r' = r, r_out,
+ *             w_post, gate and rstd_post are NULL and w_pre is not.
+ * Limits: d % 8 == 0, 8 <= d <= 8192, T >= 0 (with T == 0 the arrays sized by T
+ * may be NULL).
+ */
+typedef struct {
+  int32_t T, d, gate_group;
+  tw_dtype y_dtype, r_dtype, n_dtype, w_dtype;
+  float res_scale, block_scale, eps;
+  const void* w_post;
+  const void* gate;
+  const void* w_pre;
+} tw_norm_block;
+
+/*
+ * y [T][d] (y_dtype), r and r_out [T][d] (r_dtype), n_out [T][d] (n_dtype).
+ * rstd_post, rstd_pre [T] fp32: kept for the backward, NULL for inference.
+ * An output may share its whole array with an input of the same dtype (r_out
+ * with r, n_out with y); other overlaps are not allowed.
+ */
+TW_API tw_status norm_residual_forward(const tw_norm_block* b, const void* y, const void* r,
+                                       void* r_out, void* n_out, float* rstd_post,
+                                       float* rstd_pre, cudaStream_t stream);
+
+/*
+ * Gradients of norm_residual_forward.  dn (n_dtype) and dr_out (r_dtype) are
+ * the gradients of n and r'; dr_out may be NULL (zero), dn is NULL exactly when
+ * w_pre is.  r_out and y are the forward's, rstd_* what it kept (NULL where
+ * the norm is absent).  With rh = r' rstd_pre, yh = y rstd_post (y without a norm):
+ *   e  = dn w_pre;  G = dr_out + rstd_pre (e - rh mean(e rh));  dr = res_scale G
+ *   k  = block_scale gate[q] G;  f = k w_post;  dy = rstd_post (f - yh mean(f yh))
+ *        (dy = k without w_post)
+ *   dw_pre = sum_t dn rh;  dw_post = sum_t k yh;  dgate[q] = sum block_scale G o
+ * dr (r_dtype), dy (y_dtype); dw_post, dw_pre [d] and dgate [rows][d] fp32,
+ * fully overwritten, summed in a fixed order (deterministic).  Without y, dy,
+ * dgate and dw_post are NULL and dr = G.  dr may be dr_out, dy may be y or dn
+ * (same dtype); other overlaps are not allowed.
+ * ws: at least norm_residual_backward_workspace_size(T, d, gate_group) bytes
+ * (gate_group 0 without a gate), asked with the device current that runs the call; calls sharing
+ * one workspace must not overlap on the device.
+ */
+TW_API size_t norm_residual_backward_workspace_size(int32_t T, int32_t d, int32_t gate_group);
+TW_API tw_status norm_residual_backward(const tw_norm_block* b, const void* dn, const void* dr_out,
+                                        const void* y, const void* r_out, const float* rstd_post,
+                                        const float* rstd_pre, void* dy, void* dr, float* dw_post,
+                                        float* dgate, float* dw_pre, void* ws, size_t ws_bytes,
+                                        cudaStream_t stream);
+
+/*
  * Multi-tensor AdamW step, for the weights the training calls give gradients
  * of.  One tensor of a step, n elements, contiguous:
  *   p        the parameter (p_dtype), updated; with a master copy it receives

@@ -1,4 +1,5 @@
-"""fp64 numpy oracle of the operators around the FFN: AdamW with fp32 or 8-bit
+"""fp64 numpy oracle of the operators around the FFN: the norms before and after a
+block with its gate and residual sum, and AdamW with fp32 or 8-bit
 moments.  Test infrastructure only; written from the formulas."""
 import numpy as np
 
@@ -43,3 +44,54 @@ def adamw(p, g, m, v, *, lr, beta1, beta2, eps, step, weight_decay=0.0, grad_sca
     size = lr / (1 - beta1 ** step)
     terms = size * (np.abs(beta1 * m) + np.abs((1 - beta1) * g)) / den
     return p * (1 - lr * weight_decay) - size * m_new / den, m_new, v_new, terms
+
+
+def norm_forward(y, r, w_post, gate, w_pre, *, gate_group=0, a=1.0, s=1.0, eps=1e-6):
+    """r', n and the rows' inverse norms; None where an argument is None."""
+    T = r.shape[0]
+    p = q = n = None
+    if y is None:
+        out = r
+    else:
+        o = y
+        if w_post is not None:
+            p = 1 / np.sqrt(np.mean(y * y, axis=1) + eps)
+            o = y * p[:, None] * w_post
+        if gate is not None:
+            o = gate[np.arange(T) // gate_group] * o
+        out = a * r + s * o
+    if w_pre is not None:
+        q = 1 / np.sqrt(np.mean(out * out, axis=1) + eps)
+        n = out * q[:, None] * w_pre
+    return out, n, p, q
+
+
+def norm_backward(dn, dr_out, y, r_out, w_post, gate, w_pre, p, q, *, gate_group=0, a=1.0, s=1.0):
+    """Gradients (dict) from the kept inverse norms p (post) and q (pre)."""
+    T, d = (r_out if r_out is not None else dr_out).shape
+    out = {}
+    G = np.zeros((T, d)) if dr_out is None else dr_out.copy()
+    if dn is not None:
+        rh = r_out * q[:, None]
+        e = dn * w_pre
+        G = G + q[:, None] * (e - rh * np.mean(e * rh, axis=1, keepdims=True))
+        out["dw_pre"] = np.sum(dn * rh, axis=0)
+    out["G"] = G
+    if y is None:
+        out["dr"] = G
+        return out
+    out["dr"] = a * G
+    row = np.arange(T) // gate_group if gate is not None else None
+    k = s * G if gate is None else s * gate[row] * G
+    yh = y if w_post is None else y * p[:, None]
+    o = yh if w_post is None else yh * w_post
+    if w_post is None:
+        out["dy"] = k
+    else:
+        f = k * w_post
+        out["dy"] = p[:, None] * (f - yh * np.mean(f * yh, axis=1, keepdims=True))
+        out["dw_post"] = np.sum(k * yh, axis=0)
+    if gate is not None:
+        out["dgate"] = np.zeros_like(gate)
+        np.add.at(out["dgate"], row, s * G * o)
+    return out
