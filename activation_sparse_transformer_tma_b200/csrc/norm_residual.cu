@@ -5,17 +5,19 @@
 //
 // Both directions read and write each element once and are bound by memory:
 // 12 bytes an element forward and 18 backward for bf16 y and n and an fp32
-// residual stream.  A team of 32 ceil(d / 256) threads holds one row in
-// registers, two groups of 4 columns a thread (4 tid and 4 (tid + team)), so every
-// access is contiguous over a warp (16 bytes a lane in fp32, 8 in bf16) and the
-// weights of a thread's columns, and in the backward their gradients, stay in
-// registers over all its rows.  A row needs two reductions over d, the second of
-// them on the first's result; the next row's loads are issued before them.
-//
-// Backward: the gradients of the weights are sums over tokens.  Each CTA sums its
-// rows in registers and over its teams in shared memory, and leaves one partial
-// row; a second kernel adds the partial rows in a fixed order.  No atomics: the
-// result does not depend on timing.
+// residual stream.
+//   * A team of 32 to 512 threads holds one row in registers, four groups of 4
+//     columns a thread (4 (tid + h team)), so every access is contiguous over a
+//     warp.  With two groups a thread, twice the team, the instructions that a row
+//     costs whatever its width (two reductions, addresses, waits) bounded the
+//     kernels: 68 instructions an element forward and 85 backward.
+//   * Rows arrive by asynchronous copies, up to three rows ahead.  The thread that
+//     copies is the thread that reads, so waiting for its own copies is all the
+//     synchronisation the ring needs.
+//   * The backward sums the weights' gradients over a CTA's rows in registers and
+//     over its teams in shared memory, and leaves one partial row; a second kernel
+//     adds the partial rows in a fixed order.  No atomics: the result does not
+//     depend on timing.
 #include "pdl.cuh"
 #include "tw_common.cuh"
 #include "tw_internal.h"
@@ -23,47 +25,139 @@
 namespace tw {
 namespace {
 
-// Four columns of a row, as loaded.
-template <bool BF>
-struct Quad;
-template <>
-struct Quad<true> {
-  uint2 w;
-  TW_DEV void load(const void* base, size_t i) {
-    w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
-  }
-  TW_DEV void zero() { w = make_uint2(0u, 0u); }
-  TW_DEV void get(float (&x)[4]) const {
-    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-  }
-};
-template <>
-struct Quad<false> {
-  float4 w;
-  TW_DEV void load(const void* base, size_t i) {
-    w = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-  }
-  TW_DEV void zero() { w = make_float4(0.f, 0.f, 0.f, 0.f); }
-  TW_DEV void get(float (&x)[4]) const { x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w; }
+constexpr int kQ = 4;  // groups of 4 columns a thread
+
+// A CTA's threads for a team size, and its teams.
+template <int TEAM>
+struct Shape {
+  static constexpr int THREADS = TEAM > 256 ? TEAM : 256;
+  static constexpr int TEAMS = THREADS / TEAM;
+  static constexpr int WARPS = TEAM / 32;
 };
 
-TW_DEV void load4(const void* base, bool bf16, size_t i, float (&x)[4]) {
+// Four columns as a thread holds them: 8 bytes in bf16, 16 in fp32.
+TW_DEV void unpack4(const uint2 w, float (&x)[4]) {
+  x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+}
+TW_DEV uint2 pack4(const float (&x)[4]) {
+  return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+}
+TW_DEV float4 vec4(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
+
+// The thread's columns of a row in global memory; i is the first group's index.
+// The type is tested once a row and array, not once a group.
+template <int TEAM>
+TW_DEV void load_row(const void* base, bool bf16, size_t i, const bool (&in)[kQ],
+                     float (&x)[kQ][4]) {
   if (bf16) {
-    Quad<true> q;
-    q.load(base, i);
-    q.get(x);
+    const uint16_t* p = static_cast<const uint16_t*>(base) + i;
+#pragma unroll
+    for (int h = 0; h < kQ; ++h)
+      if (in[h]) unpack4(*reinterpret_cast<const uint2*>(p + h * 4 * TEAM), x[h]);
   } else {
-    Quad<false> q;
-    q.load(base, i);
-    q.get(x);
+    const float* p = static_cast<const float*>(base) + i;
+#pragma unroll
+    for (int h = 0; h < kQ; ++h)
+      if (in[h]) {
+        const float4 w = *reinterpret_cast<const float4*>(p + h * 4 * TEAM);
+        x[h][0] = w.x; x[h][1] = w.y; x[h][2] = w.z; x[h][3] = w.w;
+      }
   }
 }
-TW_DEV void store4(void* base, bool bf16, size_t i, const float (&x)[4]) {
-  if (bf16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
-        make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(x[0], x[1], x[2], x[3]);
+template <int TEAM>
+TW_DEV void store_row(void* base, bool bf16, size_t i, const bool (&in)[kQ],
+                      const float (&x)[kQ][4]) {
+  if (bf16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + i;
+#pragma unroll
+    for (int h = 0; h < kQ; ++h)
+      if (in[h]) *reinterpret_cast<uint2*>(p + h * 4 * TEAM) = pack4(x[h]);
+  } else {
+    float* p = static_cast<float*>(base) + i;
+#pragma unroll
+    for (int h = 0; h < kQ; ++h)
+      if (in[h]) *reinterpret_cast<float4*>(p + h * 4 * TEAM) = vec4(x[h]);
+  }
+}
+
+// The same columns in the ring: group h of all threads, contiguous over the threads.
+template <int TEAM>
+TW_DEV void copy_row(uint32_t array, const void* base, bool bf16, size_t i,
+                     const bool (&in)[kQ]) {
+  constexpr int N = Shape<TEAM>::THREADS;
+  if (bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + i;
+    const uint32_t to = array + threadIdx.x * 8;
+#pragma unroll
+    for (int h = 0; h < kQ; ++h)
+      if (in[h])
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
+                     ::"r"(to + h * N * 8), "l"(p + h * 4 * TEAM) : "memory");
+  } else {
+    const float* p = static_cast<const float*>(base) + i;
+    const uint32_t to = array + threadIdx.x * 16;
+#pragma unroll
+    for (int h = 0; h < kQ; ++h)
+      if (in[h])
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     ::"r"(to + h * N * 16), "l"(p + h * 4 * TEAM) : "memory");
+  }
+}
+// Columns past d read what is in their place: zeros that zero_ring() left there.
+template <int TEAM>
+TW_DEV void read_row(uint32_t array, bool bf16, float (&x)[kQ][4]) {
+  constexpr int N = Shape<TEAM>::THREADS;
+  if (bf16) {
+    const uint32_t at = array + threadIdx.x * 8;
+#pragma unroll
+    for (int h = 0; h < kQ; ++h) {
+      uint2 w;
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(w.x), "=r"(w.y) : "r"(at + h * N * 8) : "memory");
+      unpack4(w, x[h]);
+    }
+  } else {
+    const uint32_t at = array + threadIdx.x * 16;
+#pragma unroll
+    for (int h = 0; h < kQ; ++h)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(x[h][0]), "=f"(x[h][1]), "=f"(x[h][2]), "=f"(x[h][3])
+                   : "r"(at + h * N * 16) : "memory");
+  }
+}
+TW_DEV void copy_float(uint32_t to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+TW_DEV float read_float(uint32_t at) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+TW_DEV void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// The oldest of `stages` groups has landed.
+TW_DEV void copies_wait(int stages) {
+  if (stages >= 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// A ring of `stages` rows: a row's copies are issued stages - 1 rows ahead, into the
+// place of the row just read (with one stage: at its own turn).  Offsets of the
+// arrays within a stage, in bytes; an absent array has no room.
+struct Ring {
+  int y, r, dr, dn, gate, p, bytes, stages;
+};
+
+// Rows narrower than the team's columns: the places past d, which no copy writes,
+// are cleared once (with the rest; the threads meet before the first copy).
+template <int TEAM>
+TW_DEV void zero_ring(uint32_t base, const Ring& ring, int d) {
+  if (d == TEAM * 4 * kQ) return;
+  const int total = ring.bytes * ring.stages;
+  for (int i = threadIdx.x * 16; i < total; i += Shape<TEAM>::THREADS * 16)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + i), "r"(0u) : "memory");
+  __syncthreads();
 }
 
 struct Block {
@@ -73,137 +167,149 @@ struct Block {
   const void *w_post, *gate, *w_pre;
 };
 
-// Threads of one row, and this thread's two groups of columns.
+// Threads of one row, and this thread's groups of columns.
+template <int TEAM>
 struct Team {
-  int size, index, tid, warps;
-  int col[2];
-  bool in[2];
-  TW_DEV Team(int d, int team_size) {
-    size = team_size;
-    index = threadIdx.x / team_size;
-    tid = threadIdx.x - index * team_size;
-    warps = team_size >> 5;
+  static constexpr int W = Shape<TEAM>::WARPS;
+  int index, tid, turn;
+  bool in[kQ];
+  TW_DEV explicit Team(int d) {
+    index = threadIdx.x / TEAM;
+    tid = threadIdx.x % TEAM;
+    turn = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      col[h] = 4 * (tid + h * team_size);
-      in[h] = col[h] < d;
-    }
+    for (int h = 0; h < kQ; ++h) in[h] = 4 * (tid + h * TEAM) < d;
   }
   // Sum over the team, in a fixed order.  `slots` holds one float per warp of the
   // CTA and alternates between two arrays: a thread that writes an array again has
   // passed the barrier of the other one, so all have read it.
-  TW_DEV float sum(float v, float (*slots)[32], int& turn) const {
+  TW_DEV float sum(float v, float (*slots)[32]) {
     v = warp_sum(v);
-    if (warps == 1) return v;
-    float* at = slots[turn] + index * warps;
+    if (W == 1) return v;
+    float* at = slots[turn] + index * W;
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) at[tid >> 5] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(size) : "memory");
+    if (TEAM == Shape<TEAM>::THREADS) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(TEAM) : "memory");
     v = 0.f;
-    for (int w = 0; w < warps; ++w) v += at[w];
+    if (W == 2) {
+      const float2 a = *reinterpret_cast<const float2*>(at);
+      return a.x + a.y;
+    }
+#pragma unroll
+    for (int w = 0; w < W / 4; ++w) {
+      const float4 a = reinterpret_cast<const float4*>(at)[w];
+      v += (a.x + a.y) + (a.z + a.w);
+    }
     return v;
   }
 };
 
-template <bool YB, bool RB>
-struct ForwardRow {
-  Quad<YB> y[2];
-  Quad<RB> r[2];
-  TW_DEV void load(const Team& tm, const void* yp, const void* rp, size_t row, int d) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      y[h].zero();
-      r[h].zero();
-      if (tm.in[h]) {
-        if (yp) y[h].load(yp, row * d + tm.col[h]);
-        r[h].load(rp, row * d + tm.col[h]);
-      }
-    }
-  }
-};
+// 1/sqrt(sum / d + eps): the approximate instruction is within 2 ulp.
+TW_DEV float inverse_norm(float sum, const Block& b) { return rsqrtf(fmaf(sum, b.inv_d, b.eps)); }
 
-template <bool YB, bool RB, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
+template <int TEAM>
+__global__ void __launch_bounds__(Shape<TEAM>::THREADS, TEAM <= 256 ? 2 : 1)
     norm_forward_kernel(const Block b, const void* y, const void* r, void* r_out, void* n_out,
-                        float* rstd_post, float* rstd_pre, int team_size) {
-  __shared__ float slots[2][32];
-  const Team tm(b.d, team_size);
-  const int teams = blockDim.x / team_size;
-  const long long stride = (long long)gridDim.x * teams;
-  long long row = (long long)blockIdx.x * teams + tm.index;
-  int turn = 0;
+                        float* rstd_post, float* rstd_pre, const Ring ring) {
+  extern __shared__ __align__(16) uint8_t rows[];
+  __shared__ __align__(16) float slots[2][32];
+  Team<TEAM> tm(b.d);
+  constexpr int TEAMS = Shape<TEAM>::TEAMS;
+  const long long stride = (long long)gridDim.x * TEAMS;
+  const long long first = (long long)blockIdx.x * TEAMS + tm.index;
+  const uint32_t base = smem_u32(rows);
+  zero_ring<TEAM>(base, ring, b.d);
   pdl_wait();
   pdl_launch_next();
-  // c = block_scale * gate * w_post of this thread's columns, kept over its rows
-  // unless tokens have gate rows of their own
-  float c[2][4], wpre[2][4];
   const bool gate_rows = b.gate && b.gate_group < b.T;
-  auto scales = [&](size_t gate_row) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (!tm.in[h]) continue;
-      float w[4] = {1.f, 1.f, 1.f, 1.f}, gt[4] = {1.f, 1.f, 1.f, 1.f};
-      if (b.w_post) load4(b.w_post, b.w_bf16, tm.col[h], w);
-      if (b.gate) load4(b.gate, b.w_bf16, gate_row * b.d + tm.col[h], gt);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) c[h][k] = b.s * gt[k] * w[k];
+  auto fetch = [&](int stage, long long row) {
+    if (row < b.T) {
+      const uint32_t to = base + stage * ring.bytes;
+      const size_t i = (size_t)row * b.d + 4 * tm.tid;
+      if (y) copy_row<TEAM>(to + ring.y, y, b.y_bf16, i, tm.in);
+      copy_row<TEAM>(to + ring.r, r, b.r_bf16, i, tm.in);
+      if (gate_rows)
+        copy_row<TEAM>(to + ring.gate, b.gate, b.w_bf16,
+                       (size_t)((int)row / b.gate_group) * b.d + 4 * tm.tid, tm.in);
     }
+    copies_commit();
   };
+  for (int k = 0; k + 1 < ring.stages; ++k) fetch(k, first + k * stride);
+
+  // c = block_scale * gate * w_post of this thread's columns; without gate rows
+  // it is kept over the thread's rows.  Columns past d: everything is zero there.
+  float c[kQ][4] = {}, wpre[kQ][4] = {};
+  if (y && !gate_rows) {
+    float gt[kQ][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kQ; ++h)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) c[h][k] = wpre[h][k] = 0.f;
-  if (y && !gate_rows) scales(0);
-  if (b.w_pre) {
+      for (int k = 0; k < 4; ++k) c[h][k] = gt[h][k] = 1.f;
+    if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, c);
+    if (b.gate) load_row<TEAM>(b.gate, b.w_bf16, 4 * tm.tid, tm.in, gt);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (tm.in[h]) load4(b.w_pre, b.w_bf16, tm.col[h], wpre[h]);
+    for (int h = 0; h < kQ; ++h)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[h][k] *= b.s * gt[h][k];
   }
-  ForwardRow<YB, RB> next;
-  if (row < b.T) next.load(tm, y, r, row, b.d);
-  for (; row < b.T; row += stride) {
-    const ForwardRow<YB, RB> cur = next;
-    if (row + stride < b.T) next.load(tm, y, r, row + stride, b.d);
-    float rv[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) cur.r[h].get(rv[h]);
+  if (b.w_pre) load_row<TEAM>(b.w_pre, b.w_bf16, 4 * tm.tid, tm.in, wpre);
+
+  int stage = 0;
+  for (long long row = first; row < b.T; row += stride) {
+    // into the stage read before
+    fetch(stage == 0 ? ring.stages - 1 : stage - 1, row + (ring.stages - 1) * stride);
+    copies_wait(ring.stages);
+    const uint32_t from = base + stage * ring.bytes;
+    if (++stage == ring.stages) stage = 0;
+    const size_t i = (size_t)row * b.d + 4 * tm.tid;
+    float rv[kQ][4];
+    read_row<TEAM>(from + ring.r, b.r_bf16, rv);
     if (y) {
-      if (gate_rows) scales((size_t)((int)row / b.gate_group));
-      float yv[2][4];
+      float yv[kQ][4];
+      read_row<TEAM>(from + ring.y, b.y_bf16, yv);
+      if (gate_rows) {
+        float w[kQ][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) cur.y[h].get(yv[h]);
+        for (int h = 0; h < kQ; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[h][k] = 1.f;
+        read_row<TEAM>(from + ring.gate, b.w_bf16, c);
+        if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
+#pragma unroll
+        for (int h = 0; h < kQ; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[h][k] *= b.s * w[h][k];
+      }
       float p = 1.f;
       if (b.w_post) {
         float ss = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kQ; ++h)
 #pragma unroll
           for (int k = 0; k < 4; ++k) ss = fmaf(yv[h][k], yv[h][k], ss);
-        p = 1.f / sqrtf(fmaf(tm.sum(ss, slots, turn), b.inv_d, b.eps));
+        p = inverse_norm(tm.sum(ss, slots), b);
         if (rstd_post && tm.tid == 0) rstd_post[row] = p;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kQ; ++h)
 #pragma unroll
         for (int k = 0; k < 4; ++k) rv[h][k] = fmaf(yv[h][k] * p, c[h][k], b.a * rv[h][k]);
-        if (tm.in[h]) store4(r_out, RB, (size_t)row * b.d + tm.col[h], rv[h]);
-      }
+      store_row<TEAM>(r_out, b.r_bf16, i, tm.in, rv);
     }
     if (b.w_pre) {
       float ss = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kQ; ++h)
 #pragma unroll
         for (int k = 0; k < 4; ++k) ss = fmaf(rv[h][k], rv[h][k], ss);
-      const float p = 1.f / sqrtf(fmaf(tm.sum(ss, slots, turn), b.inv_d, b.eps));
+      const float p = inverse_norm(tm.sum(ss, slots), b);
       if (rstd_pre && tm.tid == 0) rstd_pre[row] = p;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float nv[4];
+      for (int h = 0; h < kQ; ++h)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) nv[k] = rv[h][k] * p * wpre[h][k];
-        if (tm.in[h]) store4(n_out, b.n_bf16, (size_t)row * b.d + tm.col[h], nv);
-      }
+        for (int k = 0; k < 4; ++k) rv[h][k] *= p * wpre[h][k];
+      store_row<TEAM>(n_out, b.n_bf16, i, tm.in, rv);
     }
   }
 }
@@ -218,14 +324,6 @@ struct Items {
   bool by_team;
 };
 
-template <bool YB, bool RB, bool NB>
-struct BackwardRow {
-  Quad<YB> y[2];
-  Quad<RB> r[2], dr[2];
-  Quad<NB> dn[2];
-  float ppost, ppre;
-};
-
 struct BackwardArgs {
   const void *dn, *dr_out, *y, *r_out;
   const float *rstd_post, *rstd_pre;
@@ -235,36 +333,32 @@ struct BackwardArgs {
   float* part_pre;   // [CTAs][d]
 };
 
-template <bool YB, bool RB, bool NB, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1)
-    norm_backward_kernel(const Block b, const BackwardArgs g, const Items it, int team_size) {
-  __shared__ float slots[2][32];
-  __shared__ float4 comb[MAXT * 2];  // the other teams' sums of one vector
-  const Team tm(b.d, team_size);
-  const int teams = blockDim.x / team_size;
-  const int units = it.by_team ? gridDim.x * teams : gridDim.x;
-  const int unit = it.by_team ? blockIdx.x * teams + tm.index : blockIdx.x;
-  const int first = it.by_team ? 0 : tm.index;   // this team's first row of an item
-  const int stride = it.by_team ? 1 : teams;
-  int turn = 0;
+// Shared memory behind the ring, in floats a thread: w_pre of its columns, the sums
+// of dw_post over the items done, and (teams but the first) what the first adds up.
+struct Extra {
+  int wpre, post, comb;  // byte offsets
+};
+
+// Over an item the gate is one row, so one sum A = sum_t G yh serves both the gate
+// and w_post: dgate = s w_post A and dw_post += s gate A.
+template <int TEAM>
+__global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
+    norm_backward_kernel(const Block b, const BackwardArgs g, const Items it, const Ring ring,
+                         const Extra extra) {
+  extern __shared__ __align__(16) uint8_t rows[];
+  __shared__ __align__(16) float slots[2][32];
+  Team<TEAM> tm(b.d);
+  constexpr int TEAMS = Shape<TEAM>::TEAMS, N = Shape<TEAM>::THREADS;
+  const int units = it.by_team ? gridDim.x * TEAMS : gridDim.x;
+  const int unit = it.by_team ? blockIdx.x * TEAMS + tm.index : blockIdx.x;
+  const int first = it.by_team ? 0 : tm.index;  // this team's first row of an item
+  const int stride = it.by_team ? 1 : TEAMS;
+  const uint32_t base = smem_u32(rows);
+  const bool gate_rows = b.gate && it.group < b.T;
+  const bool gate_ring = gate_rows && ring.gate >= 0;
+  zero_ring<TEAM>(base, ring, b.d);
   pdl_wait();
   pdl_launch_next();
-
-  float wpost[2][4], wpre[2][4], gate[2][4];
-  float apost[2][4], apre[2][4], agate[2][4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      wpost[h][k] = gate[h][k] = 1.f;
-      wpre[h][k] = apost[h][k] = apre[h][k] = agate[h][k] = 0.f;
-    }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (tm.in[h]) {
-      if (b.w_post) load4(b.w_post, b.w_bf16, tm.col[h], wpost[h]);
-      if (b.w_pre) load4(b.w_pre, b.w_bf16, tm.col[h], wpre[h]);
-    }
 
   auto range = [&](int item, int& row0, int& row1) {
     const int group = item / it.per_group, part = item - group * it.per_group;
@@ -276,164 +370,217 @@ __global__ void __launch_bounds__(MAXT, 1)
     row0 = (int)r0;
     row1 = (int)(r0 + it.rows_per_item < g1 ? r0 + it.rows_per_item : g1);
   };
-  using Row = BackwardRow<YB, RB, NB>;
-  auto load = [&](Row& w, int row) {
-    const size_t at = (size_t)row * b.d;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      w.y[h].zero();
-      w.r[h].zero();
-      w.dr[h].zero();
-      w.dn[h].zero();
-      if (tm.in[h]) {
-        const size_t i = at + tm.col[h];
-        if (g.y) w.y[h].load(g.y, i);
-        if (g.dn) {
-          w.dn[h].load(g.dn, i);
-          w.r[h].load(g.r_out, i);
-        }
-        if (g.dr_out) w.dr[h].load(g.dr_out, i);
+  // The row to copy next: this team's rows of its items in order, `ring.stages - 1`
+  // rows ahead of the one in hand.
+  long long ahead_item = unit, ahead_row = 0;
+  int ahead_end = 0;
+  bool ahead_new = true;  // at the first row of an item
+  auto seek = [&]() {     // the first item from ahead_item on that has a row for this team
+    for (; ahead_item < it.count; ahead_item += units) {
+      int n0;
+      range((int)ahead_item, n0, ahead_end);
+      ahead_row = (long long)n0 + first;
+      if (ahead_row < ahead_end) break;
+    }
+    ahead_new = true;
+  };
+  auto fetch = [&](int stage) {
+    if (ahead_item < it.count) {
+      const uint32_t to = base + stage * ring.bytes;
+      const size_t i = (size_t)ahead_row * b.d + 4 * tm.tid;
+      if (g.dn) {
+        copy_row<TEAM>(to + ring.dn, g.dn, b.n_bf16, i, tm.in);
+        copy_row<TEAM>(to + ring.r, g.r_out, b.r_bf16, i, tm.in);
+      }
+      if (g.dr_out) copy_row<TEAM>(to + ring.dr, g.dr_out, b.r_bf16, i, tm.in);
+      if (g.y) copy_row<TEAM>(to + ring.y, g.y, b.y_bf16, i, tm.in);
+      if (gate_ring && ahead_new)
+        copy_row<TEAM>(to + ring.gate, b.gate, b.w_bf16,
+                       (size_t)((int)ahead_item / it.per_group) * b.d + 4 * tm.tid, tm.in);
+      if (g.rstd_post) copy_float(to + ring.p + threadIdx.x * 4, g.rstd_post + ahead_row);
+      if (g.rstd_pre) copy_float(to + ring.p + (N + threadIdx.x) * 4, g.rstd_pre + ahead_row);
+      ahead_new = false;
+      ahead_row += stride;
+      if (ahead_row >= ahead_end) {
+        ahead_item += units;
+        seek();
       }
     }
-    w.ppost = g.rstd_post ? g.rstd_post[row] : 1.f;
-    w.ppre = g.rstd_pre ? g.rstd_pre[row] : 0.f;
+    copies_commit();
+  };
+  seek();
+  for (int k = 0; k + 1 < ring.stages; ++k) fetch(k);
+
+  auto ones = [&](float (&x)[kQ][4]) {
+#pragma unroll
+    for (int h = 0; h < kQ; ++h)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[h][k] = tm.in[h] ? 1.f : 0.f;
+  };
+  // A thread's own floats behind the ring.
+  auto mine = [&](int array, int h) {
+    return reinterpret_cast<float4*>(rows + array) + h * N + threadIdx.x;
   };
   // Adds a vector over the teams into the first team's registers (all threads).
-  auto combine = [&](float (&v)[2][4]) {
-    if (teams == 1) return;
+  auto combine = [&](float (&v)[kQ][4]) {
+    if (TEAMS == 1) return;
+    float4* comb = reinterpret_cast<float4*>(rows + extra.comb);
     __syncthreads();
     if (tm.index > 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        comb[((tm.index - 1) * team_size + tm.tid) * 2 + h] =
-            make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
+      for (int h = 0; h < kQ; ++h) comb[h * N + threadIdx.x - TEAM] = vec4(v[h]);
     }
     __syncthreads();
     if (tm.index == 0)
-      for (int t = 0; t + 1 < teams; ++t)
+      for (int t = 0; t + 1 < TEAMS; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 o = comb[(t * team_size + tm.tid) * 2 + h];
+        for (int h = 0; h < kQ; ++h) {
+          const float4 o = comb[h * N + t * TEAM + tm.tid];
           v[h][0] += o.x; v[h][1] += o.y; v[h][2] += o.z; v[h][3] += o.w;
         }
   };
 
-  Row next;
-  bool have = false;  // `next` holds the row that comes next
+  if (b.w_pre) {
+    float w[kQ][4] = {};
+    load_row<TEAM>(b.w_pre, b.w_bf16, 4 * tm.tid, tm.in, w);
+#pragma unroll
+    for (int h = 0; h < kQ; ++h) *mine(extra.wpre, h) = vec4(w[h]);
+  }
+  if (g.part_post) {
+#pragma unroll
+    for (int h = 0; h < kQ; ++h) *mine(extra.post, h) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float apre[kQ][4] = {}, A[kQ][4] = {}, F[kQ][4];  // F = s gate w_post
+  int stage = 0;
   for (long long next_item = unit; next_item < it.count; next_item += units) {
     const int item = (int)next_item;
     int row0, row1;
     range(item, row0, row1);
     const int group = item / it.per_group;
-    if (b.gate) {
+    const size_t gate_at = (size_t)group * b.d + 4 * tm.tid;
+    bool new_item = true;
+    for (long long row = (long long)row0 + first; row < row1; row += stride) {
+      fetch(stage == 0 ? ring.stages - 1 : stage - 1);  // into the stage read before
+      copies_wait(ring.stages);
+      const uint32_t from = base + stage * ring.bytes;
+      if (++stage == ring.stages) stage = 0;
+      if (new_item && g.y) {
+        float w[kQ][4];
+        ones(w);
+        ones(F);
+        if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
+        if (gate_ring) read_row<TEAM>(from + ring.gate, b.w_bf16, F);
+        else if (b.gate) load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, F);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (tm.in[h]) load4(b.gate, b.w_bf16, (size_t)group * b.d + tm.col[h], gate[h]);
-    }
-    for (long long at_row = (long long)row0 + first; at_row < row1; at_row += stride) {
-      const int row = (int)at_row;
-      if (!have) load(next, row);
-      const Row cur = next;
-      have = false;
-      if (stride < row1 - row) {
-        load(next, row + stride);
-        have = true;
-      } else if (units < it.count - item) {
-        int n0, n1;
-        range(item + units, n0, n1);
-        if (first < n1 - n0) {
-          load(next, n0 + first);
-          have = true;
-        }
+        for (int h = 0; h < kQ; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) F[h][k] *= b.s * w[h][k];
       }
-      float G[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) cur.dr[h].get(G[h]);
+      new_item = false;
+      const size_t i = (size_t)row * b.d + 4 * tm.tid;
+      float G[kQ][4] = {};
+      if (g.dr_out) read_row<TEAM>(from + ring.dr, b.r_bf16, G);
       if (g.dn) {
-        float dn[2][4], rh[2][4];
+        float e[kQ][4], rh[kQ][4];
+        const float p = read_float(from + ring.p + (N + threadIdx.x) * 4);
+        read_row<TEAM>(from + ring.dn, b.n_bf16, e);
+        read_row<TEAM>(from + ring.r, b.r_bf16, rh);
         float inner = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          cur.dn[h].get(dn[h]);
-          cur.r[h].get(rh[h]);
+        for (int h = 0; h < kQ; ++h) {
+          const float4 w4 = *mine(extra.wpre, h);
+          const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            rh[h][k] *= cur.ppre;
-            apre[h][k] = fmaf(dn[h][k], rh[h][k], apre[h][k]);
-            dn[h][k] *= wpre[h][k];
-            inner = fmaf(dn[h][k], rh[h][k], inner);
+            rh[h][k] *= p;
+            apre[h][k] = fmaf(e[h][k], rh[h][k], apre[h][k]);
+            e[h][k] *= w[k];
+            inner = fmaf(e[h][k], rh[h][k], inner);
           }
         }
-        inner = tm.sum(inner, slots, turn) * b.inv_d;
+        inner = tm.sum(inner, slots) * b.inv_d;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kQ; ++h)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            G[h][k] = fmaf(cur.ppre, fmaf(-rh[h][k], inner, dn[h][k]), G[h][k]);
-      }
-      const size_t at = (size_t)row * b.d;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float out[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = b.a * G[h][k];
-        if (tm.in[h]) store4(g.dr, RB, at + tm.col[h], out);
+            G[h][k] = fmaf(p, fmaf(-rh[h][k], inner, e[h][k]), G[h][k]);
       }
       if (g.dy) {
-        float yh[2][4], f[2][4];
+        float out[kQ][4];
+#pragma unroll
+        for (int h = 0; h < kQ; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) out[h][k] = b.a * G[h][k];
+        store_row<TEAM>(g.dr, b.r_bf16, i, tm.in, out);
+        float yh[kQ][4];
+        read_row<TEAM>(from + ring.y, b.y_bf16, yh);
+        const float p = b.w_post ? read_float(from + ring.p + threadIdx.x * 4) : 1.f;
         float inner = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          cur.y[h].get(yh[h]);
+        for (int h = 0; h < kQ; ++h)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            yh[h][k] *= cur.ppost;
-            const float sg = b.s * G[h][k], kk = sg * gate[h][k];
-            agate[h][k] = fmaf(sg, yh[h][k] * wpost[h][k], agate[h][k]);
-            apost[h][k] = fmaf(kk, yh[h][k], apost[h][k]);
-            f[h][k] = kk * wpost[h][k];
-            inner = fmaf(f[h][k], yh[h][k], inner);
+            yh[h][k] *= p;
+            A[h][k] = fmaf(G[h][k], yh[h][k], A[h][k]);
+            G[h][k] *= F[h][k];
+            inner = fmaf(G[h][k], yh[h][k], inner);
           }
-        }
         if (b.w_post) {
-          inner = tm.sum(inner, slots, turn) * b.inv_d;
+          inner = tm.sum(inner, slots) * b.inv_d;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < kQ; ++h)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f[h][k] = cur.ppost * fmaf(-yh[h][k], inner, f[h][k]);
+            for (int k = 0; k < 4; ++k) G[h][k] = p * fmaf(-yh[h][k], inner, G[h][k]);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (tm.in[h]) store4(g.dy, YB, at + tm.col[h], f[h]);
+        store_row<TEAM>(g.dy, b.y_bf16, i, tm.in, G);
+      } else {
+        store_row<TEAM>(g.dr, b.r_bf16, i, tm.in, G);  // no block and no residual scale
       }
     }
-    if (b.gate) {
-      if (!it.by_team) combine(agate);
+    if (b.gate || g.part_post) {
+      if (!it.by_team) combine(A);
       if (it.by_team || tm.index == 0) {
-        float* to = g.dgate + (size_t)(it.per_group == 1 ? group : item) * b.d;
+        float w[kQ][4], gt[kQ][4];
+        ones(w);
+        ones(gt);
+        if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
+        if (b.gate) load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, gt);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (tm.in[h]) store4(to, false, tm.col[h], agate[h]);
+        for (int h = 0; h < kQ; ++h) {
+          if (g.part_post) {
+            float4 o = *mine(extra.post, h);
+            o.x = fmaf(b.s * gt[h][0], A[h][0], o.x);
+            o.y = fmaf(b.s * gt[h][1], A[h][1], o.y);
+            o.z = fmaf(b.s * gt[h][2], A[h][2], o.z);
+            o.w = fmaf(b.s * gt[h][3], A[h][3], o.w);
+            *mine(extra.post, h) = o;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[h][k] *= b.s * A[h][k];
+        }
+        if (b.gate)
+          store_row<TEAM>(g.dgate + (size_t)(it.per_group == 1 ? group : item) * b.d, false,
+                          4 * tm.tid, tm.in, w);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kQ; ++h)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) agate[h][k] = 0.f;
+        for (int k = 0; k < 4; ++k) A[h][k] = 0.f;
     }
   }
+  const size_t part_at = (size_t)blockIdx.x * b.d + 4 * tm.tid;
   if (g.part_pre) {
     combine(apre);
-    if (tm.index == 0)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (tm.in[h]) store4(g.part_pre + (size_t)blockIdx.x * b.d, false, tm.col[h], apre[h]);
+    if (tm.index == 0) store_row<TEAM>(g.part_pre, false, part_at, tm.in, apre);
   }
   if (g.part_post) {
-    combine(apost);
-    if (tm.index == 0)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (tm.in[h]) store4(g.part_post + (size_t)blockIdx.x * b.d, false, tm.col[h], apost[h]);
+    for (int h = 0; h < kQ; ++h) {
+      const float4 o = *mine(extra.post, h);
+      A[h][0] = o.x; A[h][1] = o.y; A[h][2] = o.z; A[h][3] = o.w;
+    }
+    combine(A);
+    if (tm.index == 0) store_row<TEAM>(g.part_post, false, part_at, tm.in, A);
   }
 }
 
@@ -478,7 +625,12 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const RowSums 
   }
 }
 
-int team_size_of(int d) { return 32 * ((d + 255) / 256); }
+int team_size_of(int d) {
+  int team = 32;
+  while (team * 4 * kQ < d) team *= 2;
+  return team;
+}
+int threads_of(int team) { return team > 256 ? team : 256; }
 
 // The backward's launch: CTAs, and how rows are dealt out.  The same rule sizes the
 // workspace, from T, d and gate_group alone (sms: the SMs of the current device).
@@ -486,7 +638,6 @@ struct Plan {
   Items it;
   int ctas, threads, team;
 };
-constexpr int kBwdThreads = 512;
 // Groups shorter than this go to one team each: a CTA's teams would share too few
 // rows of one, and meet at a barrier after each.
 constexpr int kShortGroup = 32;
@@ -494,8 +645,8 @@ constexpr int kShortGroup = 32;
 Plan make_plan(int T, int d, int gate_group, int sms) {
   Plan p;
   p.team = team_size_of(d);
-  const int teams = p.team >= kBwdThreads ? 1 : kBwdThreads / p.team;
-  p.threads = teams * p.team;
+  p.threads = threads_of(p.team);
+  const int teams = p.threads / p.team;
   const long long T64 = T;
   const int group = gate_group <= 0 || gate_group > T ? (T > 0 ? T : 1) : gate_group;
   const int groups = (int)((T64 + group - 1) / group);
@@ -507,13 +658,13 @@ Plan make_plan(int T, int d, int gate_group, int sms) {
   } else {
     // enough items for every SM; an item has a row for each team at least
     long long per = groups >= sms ? 1 : (sms + groups - 1) / groups;
-    const long long most = (group + teams - 1) / teams;
+    const long long most = (group + (long long)teams - 1) / teams;
     if (per > most) per = most;
     p.it.rows_per_item = (int)((group + per - 1) / per);
-    p.it.per_group = (group + p.it.rows_per_item - 1) / p.it.rows_per_item;
+    p.it.per_group = (int)((group + (long long)p.it.rows_per_item - 1) / p.it.rows_per_item);
   }
   p.it.count = groups * p.it.per_group;
-  const int units = p.it.by_team ? (p.it.count + teams - 1) / teams : p.it.count;
+  const int units = (int)(p.it.by_team ? ((long long)p.it.count + teams - 1) / teams : p.it.count);
   p.ctas = units < sms ? units : sms;
   return p;
 }
@@ -554,29 +705,76 @@ Block device_block(const tw_norm_block& b) {
   return k;
 }
 
-template <bool YB, bool RB>
-cudaError_t forward_dtyped(const Block& k, const void* y, const void* r, void* r_out, void* n_out,
-                           float* rstd_post, float* rstd_pre, cudaStream_t stream) {
-  const int team = team_size_of(k.d);
-  const int teams = team >= 256 ? 1 : 256 / team;
-  const long long want = ((long long)k.T + teams - 1) / teams;
-  const long long most = (long long)num_sms() * (team <= 256 ? 3 : 1024 / team);
-  const dim3 grid((unsigned)(want < most ? want : most)), block(teams * team);
-  if (team <= 256)
-    return launch_pdl(norm_forward_kernel<YB, RB, 256>, grid, block, 0, stream, k, y, r, r_out,
-                      n_out, rstd_post, rstd_pre, team);
-  return launch_pdl(norm_forward_kernel<YB, RB, 1024>, grid, block, 0, stream, k, y, r, r_out,
-                    n_out, rstd_post, rstd_pre, team);
+// Shared memory of an SM for the rings, beside 1 KB a CTA that the system takes and
+// the kernels' own arrays.
+constexpr int kSmemSm = 224 * 1024;
+
+// The ring for the arrays that a call has (bytes of an element, 0 if absent).
+Ring make_ring(int threads, int y, int r, int dr, int dn, int gate, bool p, int room) {
+  Ring q;
+  int at = 0;
+  auto take = [&](int size) {
+    const int here = size ? at : -1;
+    at += 4 * kQ * threads * size;
+    return here;
+  };
+  q.y = take(y);
+  q.r = take(r);
+  q.dr = take(dr);
+  q.dn = take(dn);
+  q.gate = take(gate);
+  q.p = at;
+  if (p) at += 2 * threads * 4;
+  q.bytes = at;
+  q.stages = room / at < 1 ? 1 : room / at > 4 ? 4 : room / at;
+  return q;
 }
 
-template <bool YB, bool RB, bool NB>
-cudaError_t backward_dtyped(const Block& k, const BackwardArgs& g, const Plan& p,
-                            cudaStream_t stream) {
-  if (p.threads <= kBwdThreads)
-    return launch_pdl(norm_backward_kernel<YB, RB, NB, kBwdThreads>, dim3(p.ctas),
-                      dim3(p.threads), 0, stream, k, g, p.it, p.team);
-  return launch_pdl(norm_backward_kernel<YB, RB, NB, 1024>, dim3(p.ctas), dim3(p.threads), 0,
-                    stream, k, g, p.it, p.team);
+template <int TEAM>
+cudaError_t forward_team(const Block& k, const void* y, const void* r, void* r_out, void* n_out,
+                         float* rstd_post, float* rstd_pre, cudaStream_t stream) {
+  using S = Shape<TEAM>;
+  constexpr int per_sm = TEAM <= 256 ? 2 : 1;
+  const long long want = ((long long)k.T + S::TEAMS - 1) / S::TEAMS;
+  const long long most = (long long)num_sms() * per_sm;
+  const bool gate_rows = k.gate && k.gate_group < k.T;
+  const int w = k.w_bf16 ? 2 : 4;
+  const Ring ring = make_ring(S::THREADS, !y ? 0 : k.y_bf16 ? 2 : 4, k.r_bf16 ? 2 : 4, 0, 0,
+                              gate_rows ? w : 0, false, kSmemSm / per_sm - 1024);
+  const size_t smem = (size_t)ring.bytes * ring.stages;
+  cudaError_t e =
+      set_smem_limit(reinterpret_cast<const void*>(norm_forward_kernel<TEAM>), (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_forward_kernel<TEAM>, dim3((unsigned)(want < most ? want : most)),
+                    dim3(S::THREADS), smem, stream, k, y, r, r_out, n_out, rstd_post, rstd_pre,
+                    ring);
+}
+
+template <int TEAM>
+cudaError_t backward_team(const Block& k, const BackwardArgs& g, const Plan& p,
+                          cudaStream_t stream) {
+  using S = Shape<TEAM>;
+  const int r = k.r_bf16 ? 2 : 4, w = k.w_bf16 ? 2 : 4;
+  const bool gate_rows = k.gate && p.it.group < k.T;
+  const int vector = 4 * 4 * kQ * S::THREADS;  // fp32 columns of every thread
+  const int behind = vector * ((k.w_pre ? 1 : 0) + (g.part_post ? 1 : 0) + (S::TEAMS > 1 ? 1 : 0));
+  // the widest rows' gate rows are read when they are needed, not ahead: with fp32
+  // arrays they would not fit
+  const Ring ring = make_ring(S::THREADS, !g.y ? 0 : k.y_bf16 ? 2 : 4, g.dn ? r : 0,
+                              g.dr_out ? r : 0, !g.dn ? 0 : k.n_bf16 ? 2 : 4,
+                              gate_rows && TEAM <= 256 ? w : 0, true, kSmemSm - behind);
+  Extra x;
+  int at = ring.bytes * ring.stages;
+  x.wpre = at;
+  at += k.w_pre ? vector : 0;
+  x.post = at;
+  at += g.part_post ? vector : 0;
+  x.comb = at;
+  at += S::TEAMS > 1 ? vector : 0;
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(norm_backward_kernel<TEAM>), at);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_backward_kernel<TEAM>, dim3(p.ctas), dim3(p.threads), (size_t)at, stream,
+                    k, g, p.it, ring, x);
 }
 
 }  // namespace
@@ -585,11 +783,14 @@ cudaError_t launch_norm_forward(const tw_norm_block& b, const void* y, const voi
                                 void* n_out, float* rstd_post, float* rstd_pre,
                                 cudaStream_t stream) {
   const Block k = device_block(b);
-  if (k.y_bf16)
-    return k.r_bf16 ? forward_dtyped<true, true>(k, y, r, r_out, n_out, rstd_post, rstd_pre, stream)
-                    : forward_dtyped<true, false>(k, y, r, r_out, n_out, rstd_post, rstd_pre, stream);
-  return k.r_bf16 ? forward_dtyped<false, true>(k, y, r, r_out, n_out, rstd_post, rstd_pre, stream)
-                  : forward_dtyped<false, false>(k, y, r, r_out, n_out, rstd_post, rstd_pre, stream);
+  auto run = [&](auto f) { return f(k, y, r, r_out, n_out, rstd_post, rstd_pre, stream); };
+  switch (team_size_of(b.d)) {
+    case 32: return run(forward_team<32>);
+    case 64: return run(forward_team<64>);
+    case 128: return run(forward_team<128>);
+    case 256: return run(forward_team<256>);
+    default: return run(forward_team<512>);
+  }
 }
 
 size_t norm_backward_ws_bytes(int T, int d, int gate_group) {
@@ -618,16 +819,12 @@ cudaError_t launch_norm_backward(const tw_norm_block& b, const void* dn, const v
   const bool gate_parts = dgate && p.it.per_group > 1;
   g.dgate = gate_parts ? at(q.gate) : dgate;
   cudaError_t e;
-  const int kind = (k.y_bf16 ? 4 : 0) | (k.r_bf16 ? 2 : 0) | (k.n_bf16 ? 1 : 0);
-  switch (kind) {
-    case 0: e = backward_dtyped<false, false, false>(k, g, p, stream); break;
-    case 1: e = backward_dtyped<false, false, true>(k, g, p, stream); break;
-    case 2: e = backward_dtyped<false, true, false>(k, g, p, stream); break;
-    case 3: e = backward_dtyped<false, true, true>(k, g, p, stream); break;
-    case 4: e = backward_dtyped<true, false, false>(k, g, p, stream); break;
-    case 5: e = backward_dtyped<true, false, true>(k, g, p, stream); break;
-    case 6: e = backward_dtyped<true, true, false>(k, g, p, stream); break;
-    default: e = backward_dtyped<true, true, true>(k, g, p, stream); break;
+  switch (p.team) {
+    case 32: e = backward_team<32>(k, g, p, stream); break;
+    case 64: e = backward_team<64>(k, g, p, stream); break;
+    case 128: e = backward_team<128>(k, g, p, stream); break;
+    case 256: e = backward_team<256>(k, g, p, stream); break;
+    default: e = backward_team<512>(k, g, p, stream); break;
   }
   if (e != cudaSuccess) return e;
   RowSums s;
