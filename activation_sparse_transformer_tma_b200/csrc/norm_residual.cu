@@ -27,13 +27,11 @@ namespace {
 
 constexpr int kQ = 4;  // groups of 4 columns a thread
 
-// A CTA's threads for a team size, and its teams.
-template <int TEAM>
-struct Shape {
-  static constexpr int THREADS = TEAM > 256 ? TEAM : 256;
-  static constexpr int TEAMS = THREADS / TEAM;
-  static constexpr int WARPS = TEAM / 32;
-};
+// Threads of a CTA for a team size.  Forward: two CTAs of 256 threads on an SM at 128
+// registers.  Backward: one CTA, of 384 threads at 168 registers where several teams
+// fit in it.
+constexpr int fwd_threads(int team) { return team > 256 ? team : 256; }
+constexpr int bwd_threads(int team) { return team <= 128 ? 384 : team; }
 
 // Four columns as a thread holds them: 8 bytes in bf16, 16 in fp32.
 TW_DEV void unpack4(const uint2 w, float (&x)[4]) {
@@ -81,10 +79,9 @@ TW_DEV void store_row(void* base, bool bf16, size_t i, const bool (&in)[kQ],
 }
 
 // The same columns in the ring: group h of all threads, contiguous over the threads.
-template <int TEAM>
+template <int TEAM, int N>
 TW_DEV void copy_row(uint32_t array, const void* base, bool bf16, size_t i,
                      const bool (&in)[kQ]) {
-  constexpr int N = Shape<TEAM>::THREADS;
   if (bf16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + i;
     const uint32_t to = array + threadIdx.x * 8;
@@ -104,9 +101,8 @@ TW_DEV void copy_row(uint32_t array, const void* base, bool bf16, size_t i,
   }
 }
 // Columns past d read what is in their place: zeros that zero_ring() left there.
-template <int TEAM>
+template <int N>
 TW_DEV void read_row(uint32_t array, bool bf16, float (&x)[kQ][4]) {
-  constexpr int N = Shape<TEAM>::THREADS;
   if (bf16) {
     const uint32_t at = array + threadIdx.x * 8;
 #pragma unroll
@@ -151,11 +147,11 @@ struct Ring {
 
 // Rows narrower than the team's columns: the places past d, which no copy writes,
 // are cleared once (with the rest; the threads meet before the first copy).
-template <int TEAM>
+template <int TEAM, int N>
 TW_DEV void zero_ring(uint32_t base, const Ring& ring, int d) {
   if (d == TEAM * 4 * kQ) return;
   const int total = ring.bytes * ring.stages;
-  for (int i = threadIdx.x * 16; i < total; i += Shape<TEAM>::THREADS * 16)
+  for (int i = threadIdx.x * 16; i < total; i += N * 16)
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + i), "r"(0u) : "memory");
   __syncthreads();
 }
@@ -167,10 +163,10 @@ struct Block {
   const void *w_post, *gate, *w_pre;
 };
 
-// Threads of one row, and this thread's groups of columns.
-template <int TEAM>
+// Threads of one row, and this thread's groups of columns; N threads in the CTA.
+template <int TEAM, int N>
 struct Team {
-  static constexpr int W = Shape<TEAM>::WARPS;
+  static constexpr int W = TEAM / 32;
   int index, tid, turn;
   bool in[kQ];
   TW_DEV explicit Team(int d) {
@@ -180,28 +176,38 @@ struct Team {
 #pragma unroll
     for (int h = 0; h < kQ; ++h) in[h] = 4 * (tid + h * TEAM) < d;
   }
-  // Sum over the team, in a fixed order.  `slots` holds one float per warp of the
-  // CTA and alternates between two arrays: a thread that writes an array again has
-  // passed the barrier of the other one, so all have read it.
-  TW_DEV float sum(float v, float (*slots)[32]) {
-    v = warp_sum(v);
-    if (W == 1) return v;
-    float* at = slots[turn] + index * W;
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) at[tid >> 5] = v;
-    if (TEAM == Shape<TEAM>::THREADS) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(TEAM) : "memory");
-    v = 0.f;
-    if (W == 2) {
-      const float2 a = *reinterpret_cast<const float2*>(at);
-      return a.x + a.y;
-    }
+  // Sums of K values over the team, in a fixed order.  `slots` holds K floats per
+  // warp of the CTA and alternates between two arrays: a thread that writes an
+  // array again has passed the barrier of the other one, so all have read it.
+  template <int K>
+  TW_DEV void sum(float (&v)[K], float (*slots)[K * 16]) {
 #pragma unroll
-    for (int w = 0; w < W / 4; ++w) {
-      const float4 a = reinterpret_cast<const float4*>(at)[w];
-      v += (a.x + a.y) + (a.z + a.w);
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+    if (W == 1) return;
+    float* at = slots[turn] + index * (W * K);
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) at[k * W + (tid >> 5)] = v[k];
     }
-    return v;
+    if (TEAM == N) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(TEAM) : "memory");
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (W == 2) {
+        const float2 a = *reinterpret_cast<const float2*>(at + k * W);
+        v[k] = a.x + a.y;
+      } else {
+        v[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W / 4; ++w) {
+          const float4 a = reinterpret_cast<const float4*>(at + k * W)[w];
+          v[k] += (a.x + a.y) + (a.z + a.w);
+        }
+      }
+    }
   }
 };
 
@@ -209,17 +215,17 @@ struct Team {
 TW_DEV float inverse_norm(float sum, const Block& b) { return rsqrtf(fmaf(sum, b.inv_d, b.eps)); }
 
 template <int TEAM>
-__global__ void __launch_bounds__(Shape<TEAM>::THREADS, TEAM <= 256 ? 2 : 1)
+__global__ void __launch_bounds__(fwd_threads(TEAM), TEAM <= 256 ? 2 : 1)
     norm_forward_kernel(const Block b, const void* y, const void* r, void* r_out, void* n_out,
                         float* rstd_post, float* rstd_pre, const Ring ring) {
   extern __shared__ __align__(16) uint8_t rows[];
-  __shared__ __align__(16) float slots[2][32];
-  Team<TEAM> tm(b.d);
-  constexpr int TEAMS = Shape<TEAM>::TEAMS;
+  __shared__ __align__(16) float slots[2][16];
+  constexpr int N = fwd_threads(TEAM), TEAMS = N / TEAM;
+  Team<TEAM, N> tm(b.d);
   const long long stride = (long long)gridDim.x * TEAMS;
   const long long first = (long long)blockIdx.x * TEAMS + tm.index;
   const uint32_t base = smem_u32(rows);
-  zero_ring<TEAM>(base, ring, b.d);
+  zero_ring<TEAM, N>(base, ring, b.d);
   pdl_wait();
   pdl_launch_next();
   const bool gate_rows = b.gate && b.gate_group < b.T;
@@ -227,10 +233,10 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, TEAM <= 256 ? 2 : 1)
     if (row < b.T) {
       const uint32_t to = base + stage * ring.bytes;
       const size_t i = (size_t)row * b.d + 4 * tm.tid;
-      if (y) copy_row<TEAM>(to + ring.y, y, b.y_bf16, i, tm.in);
-      copy_row<TEAM>(to + ring.r, r, b.r_bf16, i, tm.in);
+      if (y) copy_row<TEAM, N>(to + ring.y, y, b.y_bf16, i, tm.in);
+      copy_row<TEAM, N>(to + ring.r, r, b.r_bf16, i, tm.in);
       if (gate_rows)
-        copy_row<TEAM>(to + ring.gate, b.gate, b.w_bf16,
+        copy_row<TEAM, N>(to + ring.gate, b.gate, b.w_bf16,
                        (size_t)((int)row / b.gate_group) * b.d + 4 * tm.tid, tm.in);
     }
     copies_commit();
@@ -264,17 +270,17 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, TEAM <= 256 ? 2 : 1)
     if (++stage == ring.stages) stage = 0;
     const size_t i = (size_t)row * b.d + 4 * tm.tid;
     float rv[kQ][4];
-    read_row<TEAM>(from + ring.r, b.r_bf16, rv);
+    read_row<N>(from + ring.r, b.r_bf16, rv);
     if (y) {
       float yv[kQ][4];
-      read_row<TEAM>(from + ring.y, b.y_bf16, yv);
+      read_row<N>(from + ring.y, b.y_bf16, yv);
       if (gate_rows) {
         float w[kQ][4];
 #pragma unroll
         for (int h = 0; h < kQ; ++h)
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[h][k] = 1.f;
-        read_row<TEAM>(from + ring.gate, b.w_bf16, c);
+        read_row<N>(from + ring.gate, b.w_bf16, c);
         if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
 #pragma unroll
         for (int h = 0; h < kQ; ++h)
@@ -283,12 +289,13 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, TEAM <= 256 ? 2 : 1)
       }
       float p = 1.f;
       if (b.w_post) {
-        float ss = 0.f;
+        float ss[1] = {0.f};
 #pragma unroll
         for (int h = 0; h < kQ; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) ss = fmaf(yv[h][k], yv[h][k], ss);
-        p = inverse_norm(tm.sum(ss, slots), b);
+          for (int k = 0; k < 4; ++k) ss[0] = fmaf(yv[h][k], yv[h][k], ss[0]);
+        tm.sum(ss, slots);
+        p = inverse_norm(ss[0], b);
         if (rstd_post && tm.tid == 0) rstd_post[row] = p;
       }
 #pragma unroll
@@ -298,12 +305,13 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, TEAM <= 256 ? 2 : 1)
       store_row<TEAM>(r_out, b.r_bf16, i, tm.in, rv);
     }
     if (b.w_pre) {
-      float ss = 0.f;
+      float ss[1] = {0.f};
 #pragma unroll
       for (int h = 0; h < kQ; ++h)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ss = fmaf(rv[h][k], rv[h][k], ss);
-      const float p = inverse_norm(tm.sum(ss, slots), b);
+        for (int k = 0; k < 4; ++k) ss[0] = fmaf(rv[h][k], rv[h][k], ss[0]);
+      tm.sum(ss, slots);
+      const float p = inverse_norm(ss[0], b);
       if (rstd_pre && tm.tid == 0) rstd_pre[row] = p;
 #pragma unroll
       for (int h = 0; h < kQ; ++h)
@@ -333,22 +341,29 @@ struct BackwardArgs {
   float* part_pre;   // [CTAs][d]
 };
 
-// Shared memory behind the ring, in floats a thread: w_pre of its columns, the sums
-// of dw_post over the items done, and (teams but the first) what the first adds up.
+// Shared memory behind the ring (byte offsets): w_pre in fp32; with gate rows, each
+// thread's sums of dw_post over the items done, and (teams but the first) what the
+// first team adds up.  Without gate rows that is only done behind the loop, in the
+// ring's place.
 struct Extra {
-  int wpre, post, comb;  // byte offsets
+  int wpre, post, comb;
 };
 
 // Over an item the gate is one row, so one sum A = sum_t G yh serves both the gate
 // and w_post: dgate = s w_post A and dw_post += s gate A.
+//
+// One reduction a row: with H = dr_out + rstd_pre e, the second mean is
+//   sum f yh = sum F H yh - rstd_pre mean(e rh) sum F rh yh,   F = s gate w_post,
+// so its sums need no result of the first; a second reduction behind the first
+// took 3% longer.  The terms are those that G itself is summed from.
 template <int TEAM>
-__global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
+__global__ void __launch_bounds__(bwd_threads(TEAM), 1)
     norm_backward_kernel(const Block b, const BackwardArgs g, const Items it, const Ring ring,
                          const Extra extra) {
   extern __shared__ __align__(16) uint8_t rows[];
-  __shared__ __align__(16) float slots[2][32];
-  Team<TEAM> tm(b.d);
-  constexpr int TEAMS = Shape<TEAM>::TEAMS, N = Shape<TEAM>::THREADS;
+  __shared__ __align__(16) float slots[2][3 * 16];
+  constexpr int N = bwd_threads(TEAM), TEAMS = N / TEAM;
+  Team<TEAM, N> tm(b.d);
   const int units = it.by_team ? gridDim.x * TEAMS : gridDim.x;
   const int unit = it.by_team ? blockIdx.x * TEAMS + tm.index : blockIdx.x;
   const int first = it.by_team ? 0 : tm.index;  // this team's first row of an item
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
   const uint32_t base = smem_u32(rows);
   const bool gate_rows = b.gate && it.group < b.T;
   const bool gate_ring = gate_rows && ring.gate >= 0;
-  zero_ring<TEAM>(base, ring, b.d);
+  zero_ring<TEAM, N>(base, ring, b.d);
   pdl_wait();
   pdl_launch_next();
 
@@ -389,13 +404,13 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
       const uint32_t to = base + stage * ring.bytes;
       const size_t i = (size_t)ahead_row * b.d + 4 * tm.tid;
       if (g.dn) {
-        copy_row<TEAM>(to + ring.dn, g.dn, b.n_bf16, i, tm.in);
-        copy_row<TEAM>(to + ring.r, g.r_out, b.r_bf16, i, tm.in);
+        copy_row<TEAM, N>(to + ring.dn, g.dn, b.n_bf16, i, tm.in);
+        copy_row<TEAM, N>(to + ring.r, g.r_out, b.r_bf16, i, tm.in);
       }
-      if (g.dr_out) copy_row<TEAM>(to + ring.dr, g.dr_out, b.r_bf16, i, tm.in);
-      if (g.y) copy_row<TEAM>(to + ring.y, g.y, b.y_bf16, i, tm.in);
+      if (g.dr_out) copy_row<TEAM, N>(to + ring.dr, g.dr_out, b.r_bf16, i, tm.in);
+      if (g.y) copy_row<TEAM, N>(to + ring.y, g.y, b.y_bf16, i, tm.in);
       if (gate_ring && ahead_new)
-        copy_row<TEAM>(to + ring.gate, b.gate, b.w_bf16,
+        copy_row<TEAM, N>(to + ring.gate, b.gate, b.w_bf16,
                        (size_t)((int)ahead_item / it.per_group) * b.d + 4 * tm.tid, tm.in);
       if (g.rstd_post) copy_float(to + ring.p + threadIdx.x * 4, g.rstd_post + ahead_row);
       if (g.rstd_pre) copy_float(to + ring.p + (N + threadIdx.x) * 4, g.rstd_pre + ahead_row);
@@ -424,7 +439,7 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
   // Adds a vector over the teams into the first team's registers (all threads).
   auto combine = [&](float (&v)[kQ][4]) {
     if (TEAMS == 1) return;
-    float4* comb = reinterpret_cast<float4*>(rows + extra.comb);
+    float4* comb = reinterpret_cast<float4*>(rows + (gate_rows ? extra.comb : 0));
     __syncthreads();
     if (tm.index > 0) {
 #pragma unroll
@@ -440,13 +455,16 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
         }
   };
 
+  const bool keep_post = g.part_post && gate_rows;
+  float4* wpre = reinterpret_cast<float4*>(rows + extra.wpre) + tm.tid;
   if (b.w_pre) {
     float w[kQ][4] = {};
     load_row<TEAM>(b.w_pre, b.w_bf16, 4 * tm.tid, tm.in, w);
+    // every team writes the same values; a thread reads the columns that it wrote
 #pragma unroll
-    for (int h = 0; h < kQ; ++h) *mine(extra.wpre, h) = vec4(w[h]);
+    for (int h = 0; h < kQ; ++h) wpre[h * TEAM] = vec4(w[h]);
   }
-  if (g.part_post) {
+  if (keep_post) {
 #pragma unroll
     for (int h = 0; h < kQ; ++h) *mine(extra.post, h) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
@@ -469,7 +487,7 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
         ones(w);
         ones(F);
         if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
-        if (gate_ring) read_row<TEAM>(from + ring.gate, b.w_bf16, F);
+        if (gate_ring) read_row<N>(from + ring.gate, b.w_bf16, F);
         else if (b.gate) load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, F);
 #pragma unroll
         for (int h = 0; h < kQ; ++h)
@@ -478,66 +496,75 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
       }
       new_item = false;
       const size_t i = (size_t)row * b.d + 4 * tm.tid;
-      float G[kQ][4] = {};
-      if (g.dr_out) read_row<TEAM>(from + ring.dr, b.r_bf16, G);
-      if (g.dn) {
-        float e[kQ][4], rh[kQ][4];
-        const float p = read_float(from + ring.p + (N + threadIdx.x) * 4);
-        read_row<TEAM>(from + ring.dn, b.n_bf16, e);
-        read_row<TEAM>(from + ring.r, b.r_bf16, rh);
-        float inner = 0.f;
-#pragma unroll
-        for (int h = 0; h < kQ; ++h) {
-          const float4 w4 = *mine(extra.wpre, h);
-          const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            rh[h][k] *= p;
-            apre[h][k] = fmaf(e[h][k], rh[h][k], apre[h][k]);
-            e[h][k] *= w[k];
-            inner = fmaf(e[h][k], rh[h][k], inner);
-          }
-        }
-        inner = tm.sum(inner, slots) * b.inv_d;
-#pragma unroll
-        for (int h = 0; h < kQ; ++h)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            G[h][k] = fmaf(p, fmaf(-rh[h][k], inner, e[h][k]), G[h][k]);
-      }
+      float G[kQ][4] = {}, e[kQ][4] = {}, yh[kQ][4] = {};  // e: rh until the sums are known
+      float ppre = 0.f, ppost = 1.f;
+      float sums[3] = {0.f, 0.f, 0.f};
+      if (g.dr_out) read_row<N>(from + ring.dr, b.r_bf16, G);
       if (g.dy) {
-        float out[kQ][4];
-#pragma unroll
-        for (int h = 0; h < kQ; ++h)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) out[h][k] = b.a * G[h][k];
-        store_row<TEAM>(g.dr, b.r_bf16, i, tm.in, out);
-        float yh[kQ][4];
-        read_row<TEAM>(from + ring.y, b.y_bf16, yh);
-        const float p = b.w_post ? read_float(from + ring.p + threadIdx.x * 4) : 1.f;
-        float inner = 0.f;
-#pragma unroll
-        for (int h = 0; h < kQ; ++h)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            yh[h][k] *= p;
-            A[h][k] = fmaf(G[h][k], yh[h][k], A[h][k]);
-            G[h][k] *= F[h][k];
-            inner = fmaf(G[h][k], yh[h][k], inner);
-          }
+        read_row<N>(from + ring.y, b.y_bf16, yh);
         if (b.w_post) {
-          inner = tm.sum(inner, slots) * b.inv_d;
+          ppost = read_float(from + ring.p + threadIdx.x * 4);
 #pragma unroll
           for (int h = 0; h < kQ; ++h)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) G[h][k] = p * fmaf(-yh[h][k], inner, G[h][k]);
+            for (int k = 0; k < 4; ++k) yh[h][k] *= ppost;
         }
-        store_row<TEAM>(g.dy, b.y_bf16, i, tm.in, G);
-      } else {
-        store_row<TEAM>(g.dr, b.r_bf16, i, tm.in, G);  // no block and no residual scale
+      }
+      if (g.dn) {
+        float dn[kQ][4];
+        ppre = read_float(from + ring.p + (N + threadIdx.x) * 4);
+        read_row<N>(from + ring.dn, b.n_bf16, dn);
+        read_row<N>(from + ring.r, b.r_bf16, e);
+#pragma unroll
+        for (int h = 0; h < kQ; ++h) {
+          const float4 w4 = wpre[h * TEAM];
+          const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float rh = e[h][k] * ppre;
+            apre[h][k] = fmaf(dn[h][k], rh, apre[h][k]);
+            const float ee = dn[h][k] * w[k];
+            sums[0] = fmaf(ee, rh, sums[0]);
+            G[h][k] = fmaf(ppre, ee, G[h][k]);  // H
+            e[h][k] = rh;
+          }
+        }
+      }
+      if (b.w_post) {
+#pragma unroll
+        for (int h = 0; h < kQ; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float fy = F[h][k] * yh[h][k];
+            sums[1] = fmaf(G[h][k], fy, sums[1]);
+            sums[2] = fmaf(e[h][k], fy, sums[2]);
+          }
+      }
+      if (g.dn || b.w_post) tm.sum(sums, slots);
+      const float c = ppre * (sums[0] * b.inv_d);
+      float out[kQ][4];
+#pragma unroll
+      for (int h = 0; h < kQ; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          G[h][k] = fmaf(-c, e[h][k], G[h][k]);
+          out[h][k] = g.dy ? b.a * G[h][k] : G[h][k];  // no residual scale without a block
+        }
+      store_row<TEAM>(g.dr, b.r_bf16, i, tm.in, out);
+      if (g.dy) {
+        const float inner = fmaf(-c, sums[2], sums[1]) * b.inv_d;
+#pragma unroll
+        for (int h = 0; h < kQ; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            A[h][k] = fmaf(G[h][k], yh[h][k], A[h][k]);
+            out[h][k] = F[h][k] * G[h][k];
+            if (b.w_post) out[h][k] = ppost * fmaf(-yh[h][k], inner, out[h][k]);
+          }
+        store_row<TEAM>(g.dy, b.y_bf16, i, tm.in, out);
       }
     }
-    if (b.gate || g.part_post) {
+    if (gate_rows) {
       if (!it.by_team) combine(A);
       if (it.by_team || tm.index == 0) {
         float w[kQ][4], gt[kQ][4];
@@ -547,7 +574,7 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
         if (b.gate) load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, gt);
 #pragma unroll
         for (int h = 0; h < kQ; ++h) {
-          if (g.part_post) {
+          if (keep_post) {
             float4 o = *mine(extra.post, h);
             o.x = fmaf(b.s * gt[h][0], A[h][0], o.x);
             o.y = fmaf(b.s * gt[h][1], A[h][1], o.y);
@@ -558,9 +585,8 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[h][k] *= b.s * A[h][k];
         }
-        if (b.gate)
-          store_row<TEAM>(g.dgate + (size_t)(it.per_group == 1 ? group : item) * b.d, false,
-                          4 * tm.tid, tm.in, w);
+        store_row<TEAM>(g.dgate + (size_t)(it.per_group == 1 ? group : item) * b.d, false,
+                        4 * tm.tid, tm.in, w);
       }
 #pragma unroll
       for (int h = 0; h < kQ; ++h)
@@ -568,12 +594,13 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
         for (int k = 0; k < 4; ++k) A[h][k] = 0.f;
     }
   }
+  // without gate rows A runs over all the CTA's rows, and gives both gradients here
   const size_t part_at = (size_t)blockIdx.x * b.d + 4 * tm.tid;
   if (g.part_pre) {
     combine(apre);
     if (tm.index == 0) store_row<TEAM>(g.part_pre, false, part_at, tm.in, apre);
   }
-  if (g.part_post) {
+  if (keep_post) {
 #pragma unroll
     for (int h = 0; h < kQ; ++h) {
       const float4 o = *mine(extra.post, h);
@@ -581,6 +608,31 @@ __global__ void __launch_bounds__(Shape<TEAM>::THREADS, 1)
     }
     combine(A);
     if (tm.index == 0) store_row<TEAM>(g.part_post, false, part_at, tm.in, A);
+  } else if (!gate_rows && (b.gate || g.part_post)) {
+    combine(A);
+    if (tm.index == 0) {
+      float w[kQ][4];
+      ones(w);
+      if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
+      if (b.gate) {
+#pragma unroll
+        for (int h = 0; h < kQ; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) F[h][k] = b.s * A[h][k] * w[h][k];
+        store_row<TEAM>(g.dgate, false, part_at, tm.in, F);
+        ones(w);
+        load_row<TEAM>(b.gate, b.w_bf16, 4 * tm.tid, tm.in, w);
+      } else {
+        ones(w);
+      }
+      if (g.part_post) {
+#pragma unroll
+        for (int h = 0; h < kQ; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) A[h][k] *= b.s * w[h][k];
+        store_row<TEAM>(g.part_post, false, part_at, tm.in, A);
+      }
+    }
   }
 }
 
@@ -613,7 +665,16 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const RowSums 
   float v = 0.f;
   if (c < a.d) {
     const float* p = s.part + (size_t)row * s.each * a.d + c;
-    for (int k = warp; k < s.each; k += kSumWarps) v += p[(size_t)k * a.d];
+    for (int k0 = warp; k0 < s.each; k0 += 8 * kSumWarps) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = k0 + j * kSumWarps;
+        x[j] = k < s.each ? p[(size_t)k * a.d] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += x[j];
+    }
   }
   sums[warp][lane] = v;
   __syncthreads();
@@ -630,7 +691,6 @@ int team_size_of(int d) {
   while (team * 4 * kQ < d) team *= 2;
   return team;
 }
-int threads_of(int team) { return team > 256 ? team : 256; }
 
 // The backward's launch: CTAs, and how rows are dealt out.  The same rule sizes the
 // workspace, from T, d and gate_group alone (sms: the SMs of the current device).
@@ -645,7 +705,7 @@ constexpr int kShortGroup = 32;
 Plan make_plan(int T, int d, int gate_group, int sms) {
   Plan p;
   p.team = team_size_of(d);
-  p.threads = threads_of(p.team);
+  p.threads = bwd_threads(p.team);
   const int teams = p.threads / p.team;
   const long long T64 = T;
   const int group = gate_group <= 0 || gate_group > T ? (T > 0 ? T : 1) : gate_group;
@@ -733,44 +793,46 @@ Ring make_ring(int threads, int y, int r, int dr, int dn, int gate, bool p, int 
 template <int TEAM>
 cudaError_t forward_team(const Block& k, const void* y, const void* r, void* r_out, void* n_out,
                          float* rstd_post, float* rstd_pre, cudaStream_t stream) {
-  using S = Shape<TEAM>;
-  constexpr int per_sm = TEAM <= 256 ? 2 : 1;
-  const long long want = ((long long)k.T + S::TEAMS - 1) / S::TEAMS;
+  constexpr int N = fwd_threads(TEAM), TEAMS = N / TEAM, per_sm = TEAM <= 256 ? 2 : 1;
+  const long long want = ((long long)k.T + TEAMS - 1) / TEAMS;
   const long long most = (long long)num_sms() * per_sm;
   const bool gate_rows = k.gate && k.gate_group < k.T;
   const int w = k.w_bf16 ? 2 : 4;
-  const Ring ring = make_ring(S::THREADS, !y ? 0 : k.y_bf16 ? 2 : 4, k.r_bf16 ? 2 : 4, 0, 0,
+  const Ring ring = make_ring(N, !y ? 0 : k.y_bf16 ? 2 : 4, k.r_bf16 ? 2 : 4, 0, 0,
                               gate_rows ? w : 0, false, kSmemSm / per_sm - 1024);
   const size_t smem = (size_t)ring.bytes * ring.stages;
   cudaError_t e =
       set_smem_limit(reinterpret_cast<const void*>(norm_forward_kernel<TEAM>), (int)smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_forward_kernel<TEAM>, dim3((unsigned)(want < most ? want : most)),
-                    dim3(S::THREADS), smem, stream, k, y, r, r_out, n_out, rstd_post, rstd_pre,
+                    dim3(N), smem, stream, k, y, r, r_out, n_out, rstd_post, rstd_pre,
                     ring);
 }
 
 template <int TEAM>
 cudaError_t backward_team(const Block& k, const BackwardArgs& g, const Plan& p,
                           cudaStream_t stream) {
-  using S = Shape<TEAM>;
+  constexpr int N = bwd_threads(TEAM), TEAMS = N / TEAM;
   const int r = k.r_bf16 ? 2 : 4, w = k.w_bf16 ? 2 : 4;
   const bool gate_rows = k.gate && p.it.group < k.T;
-  const int vector = 4 * 4 * kQ * S::THREADS;  // fp32 columns of every thread
-  const int behind = vector * ((k.w_pre ? 1 : 0) + (g.part_post ? 1 : 0) + (S::TEAMS > 1 ? 1 : 0));
+  const int vector = 4 * 4 * kQ * N;  // fp32 columns of every thread
+  const int wpre = k.w_pre ? 4 * 4 * kQ * TEAM : 0;
+  const int post = gate_rows && g.part_post ? vector : 0;
+  const int comb = gate_rows && TEAMS > 1 ? vector : 0;
   // the widest rows' gate rows are read when they are needed, not ahead: with fp32
   // arrays they would not fit
-  const Ring ring = make_ring(S::THREADS, !g.y ? 0 : k.y_bf16 ? 2 : 4, g.dn ? r : 0,
+  const Ring ring = make_ring(N, !g.y ? 0 : k.y_bf16 ? 2 : 4, g.dn ? r : 0,
                               g.dr_out ? r : 0, !g.dn ? 0 : k.n_bf16 ? 2 : 4,
-                              gate_rows && TEAM <= 256 ? w : 0, true, kSmemSm - behind);
-  Extra x;
+                              gate_rows && TEAM <= 256 ? w : 0, true,
+                              kSmemSm - wpre - post - comb);
+  // the last sums over the teams take the ring's place
   int at = ring.bytes * ring.stages;
+  if (TEAMS > 1 && at < vector) at = vector;
+  Extra x;
   x.wpre = at;
-  at += k.w_pre ? vector : 0;
-  x.post = at;
-  at += g.part_post ? vector : 0;
-  x.comb = at;
-  at += S::TEAMS > 1 ? vector : 0;
+  x.post = x.wpre + wpre;
+  x.comb = x.post + post;
+  at = x.comb + comb;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(norm_backward_kernel<TEAM>), at);
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_backward_kernel<TEAM>, dim3(p.ctas), dim3(p.threads), (size_t)at, stream,

@@ -244,14 +244,17 @@ def _check_backward(t, got, group, a, s):
     G = w["G"]
     T, d = G.shape
     g_tol = 2 * U * np.abs(G)
+    terms = np.zeros_like(G)                                 # magnitudes that G is summed from
     if e["dr_out"] is not None:
         g_tol = g_tol + U * np.abs(e["dr_out"])
+        terms = terms + np.abs(e["dr_out"])
     if e["dn"] is not None:
         q = e["q"][:, None]
         rh, ee = e["r_out"] * q, e["dn"] * e["w_pre"]
         inner = np.mean(ee * rh, axis=1, keepdims=True)
         e1 = 50 * U * np.mean(np.abs(ee * rh), axis=1, keepdims=True)
         g_tol = g_tol + q * (4 * U * np.abs(ee) + np.abs(rh) * (e1 + 4 * U * np.abs(inner)))
+        terms = terms + q * (np.abs(ee) + np.abs(rh * inner))
         # a sum over T tokens, in any order: T roundings at most, and 3 of the terms
         tol = (T + 24) * U * np.sum(np.abs(e["dn"] * rh), axis=0)
         assert np.all(np.abs(_f64(got["dw_pre"]) - w["dw_pre"]) <= tol)
@@ -273,7 +276,10 @@ def _check_backward(t, got, group, a, s):
     else:
         f, f_tol = k * e["w_post"], np.abs(e["w_post"]) * k_tol + U * np.abs(k * e["w_post"])
         inner = np.mean(f * yh, axis=1, keepdims=True)
-        e2 = np.mean(f_tol * np.abs(yh) + 50 * U * np.abs(f * yh), axis=1, keepdims=True)
+        # the mean of f yh is summed from the terms of G one by one, each product rounded as in a
+        # sum of their magnitudes
+        e2 = np.mean(f_tol * np.abs(yh) + 50 * U * np.abs(s * gt * e["w_post"] * terms * yh),
+                     axis=1, keepdims=True)
         dy_tol = e["p"][:, None] * (f_tol + 4 * U * np.abs(f) +
                                     np.abs(yh) * (e2 + 4 * U * np.abs(inner)))
         tol = np.sum(k_tol * np.abs(yh) + (T + 24) * U * np.abs(k * yh), axis=0)
