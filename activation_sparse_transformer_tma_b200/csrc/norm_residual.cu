@@ -716,8 +716,9 @@ Plan make_plan(int T, int d, int gate_group, int sms) {
     p.it.per_group = 1;
     p.it.rows_per_item = group;
   } else {
-    // enough items for every SM; an item has a row for each team at least
-    long long per = groups >= sms ? 1 : (sms + groups - 1) / groups;
+    // one item for every SM, and no second wave for a few more; an item has a row
+    // for each team at least
+    long long per = groups >= sms ? 1 : sms / groups;
     const long long most = (group + (long long)teams - 1) / teams;
     if (per > most) per = most;
     p.it.rows_per_item = (int)((group + per - 1) / per);

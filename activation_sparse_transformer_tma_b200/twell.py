@@ -156,7 +156,7 @@ def lib():
 
 
 # ------------------------------------------------------------------ helpers --
-_DTYPE_CODES = {torch.bfloat16: TW_BF16, torch.float32: TW_F32}
+_DTYPE_CODES = {torch.bfloat16: TW_BF16, torch.float32: TW_F32, None: TW_F32}  # None: absent
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -189,25 +189,43 @@ def _check(fn, code):
         raise TwellError(fn, code)
 
 
-def _same_device(tensors):
-    """The one CUDA device of the tensors (None entries skipped)."""
-    found = {t.device for t in tensors if t is not None}
-    if len(found) != 1 or next(iter(found)).type != "cuda":
-        raise ValueError("tensors passed to libtwell must be on one CUDA device")
-    return found.pop()
+def _addresses(*tensors):
+    """The index of the one CUDA device of the tensors, and their addresses (None
+    for None)."""
+    index, out = None, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        i = t.get_device()
+        if i < 0 or not t.is_contiguous():
+            raise ValueError("tensors passed to libtwell must be contiguous CUDA tensors")
+        if i != index:
+            if index is not None:
+                raise ValueError("tensors passed to libtwell must be on one device")
+            index = i
+        out.append(t.data_ptr())
+    return index, out
 
 
-def _call_on(device, fn, stream, *args):
-    """lib().<fn>(*args, stream) with `device` current, on its current stream
-    unless one is given."""
-    if stream is not None and stream.device != device:
+def _call_on(index, fn, stream, *args):
+    """lib().<fn>(*args, stream) with device `index` current, on its current
+    stream unless one is given."""
+    f = getattr(_lib or lib(), fn)
+    if stream is None:
+        # the address alone: building a Stream object costs as much as a launch
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index != index:
         raise ValueError("the stream and the tensors are on different devices")
-    f = getattr(lib(), fn)
-    if torch.cuda.current_device() == device.index:
-        _check(fn, f(*args, _stream(stream)))
     else:
-        with torch.cuda.device(device):
-            _check(fn, f(*args, _stream(stream)))
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        code = f(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            code = f(*args, raw)
+    if code != 0:
+        raise TwellError(fn, code)
 
 
 class Twell:
@@ -397,26 +415,30 @@ def dense_train_saved(ws, T, F):
     return [ws[i * part:i * part + T * F * 2].view(torch.bfloat16).view(T, F) for i in range(3)]
 
 
-def _norm_block(like, y, n, w_post, gate, w_pre, r_dtype, gate_group, res_scale, block_scale, eps):
-    """The shared descriptor of a norm call; `like` is a [T, d] tensor of it."""
-    T, d = like.shape
+def _norm_block(T, d, y_dtype, r_dtype, n_dtype, weights, addresses, gate_group, res_scale,
+                block_scale, eps):
+    """The shared descriptor of a norm call; weights and addresses of (w_post, gate, w_pre)."""
     w_dtype = None
-    for w, rows in ((w_post, 1), (gate, -(-T // gate_group) if gate_group > 0 else 0), (w_pre, 1)):
+    for k, w in enumerate(weights):
         if w is None:
             continue
+        rows = 1 if k != 1 else -(-T // gate_group) if gate_group > 0 else 0
         if w.numel() != rows * d:
             raise ValueError(f"a weight of {w.numel()} elements for {rows} rows of {d}")
-        if w_dtype is not None and w.dtype != w_dtype:
+        if w_dtype is None:
+            w_dtype = w.dtype
+        elif w.dtype != w_dtype:
             raise TypeError("w_post, gate and w_pre differ in dtype")
-        w_dtype = w.dtype
-    codes = _DTYPE_CODES
+    code = _DTYPE_CODES
     try:
-        return TwNormBlockC(T, d, gate_group, TW_F32 if y is None else codes[y.dtype],
-                            codes[r_dtype], TW_F32 if n is None else codes[n.dtype],
-                            TW_F32 if w_dtype is None else codes[w_dtype], res_scale, block_scale,
-                            eps, _ptr(w_post), _ptr(gate), _ptr(w_pre))
+        return TwNormBlockC(T, d, gate_group, code[y_dtype], code[r_dtype], code[n_dtype],
+                            code[w_dtype], res_scale, block_scale, eps, *addresses)
     except KeyError as e:
         raise TypeError(f"unsupported dtype {e.args[0]}") from None
+
+
+def _dtype_of(t):
+    return None if t is None else t.dtype
 
 
 def _same_shape(like, *tensors):
@@ -437,15 +459,16 @@ def norm_residual_forward(y, r, w_post, gate, w_pre, r_out, n_out, *, gate_group
     token of [T, d] tensors.  w_post, w_pre [d], gate [ceil(T / gate_group), d]; any of them may
     be None, and y and r_out for the first norm of a network.  rstd_post, rstd_pre [T] fp32 keep
     what norm_residual_backward needs."""
-    device = _same_device((y, r, w_post, gate, w_pre, r_out, n_out, rstd_post, rstd_pre))
+    index, (yp, rp, wpost, gp, wpre, rop, nop, pp, qp) = _addresses(
+        y, r, w_post, gate, w_pre, r_out, n_out, rstd_post, rstd_pre)
     _same_shape(r, y, r_out, n_out)
     if r_out is not None and r_out.dtype != r.dtype:
         raise TypeError("r and r_out differ in dtype")
-    _floats(r.shape[0], rstd_post, rstd_pre)
-    b = _norm_block(r, y, n_out, w_post, gate, w_pre, r.dtype, gate_group, res_scale, block_scale,
-                    eps)
-    _call_on(device, "norm_residual_forward", stream, ctypes.byref(b), _ptr(y), _ptr(r),
-             _ptr(r_out), _ptr(n_out), _ptr(rstd_post), _ptr(rstd_pre))
+    T, d = r.shape
+    _floats(T, rstd_post, rstd_pre)
+    b = _norm_block(T, d, _dtype_of(y), r.dtype, _dtype_of(n_out), (w_post, gate, w_pre),
+                    (wpost, gp, wpre), gate_group, res_scale, block_scale, eps)
+    _call_on(index, "norm_residual_forward", stream, ctypes.byref(b), yp, rp, rop, nop, pp, qp)
 
 
 def norm_residual_backward_workspace_size(T, d, gate_group=0):
@@ -465,21 +488,22 @@ def norm_residual_backward(dn, dr_out, y, r_out, w_post, gate, w_pre, rstd_post,
     """Gradients of norm_residual_forward: dy, dr [T, d], dw_post, dw_pre [d] and dgate like gate
     (fp32), from dn and dr_out, the gradients of n_out and r_out (either may be None; dn is None
     exactly when w_pre is)."""
-    device = _same_device((dn, dr_out, y, r_out, w_post, gate, w_pre, rstd_post, rstd_pre, dy, dr,
-                           dw_post, dgate, dw_pre, ws))
+    index, (dnp, drop, yp, rop, wpost, gp, wpre, pp, qp, dyp, drp, dwpost, dgp, dwpre, wsp) = \
+        _addresses(dn, dr_out, y, r_out, w_post, gate, w_pre, rstd_post, rstd_pre, dy, dr, dw_post,
+                   dgate, dw_pre, ws)
     _same_shape(dr, dn, dr_out, y, r_out, dy)
     for a, b in ((dr_out, dr), (r_out, dr), (dy, y)):
         if a is not None and b is not None and a.dtype != b.dtype:
             raise TypeError("a gradient differs in dtype from its tensor")
-    _floats(dr.shape[0], rstd_post, rstd_pre)
-    _floats(dr.shape[1], dw_post, dw_pre)
+    T, d = dr.shape
+    _floats(T, rstd_post, rstd_pre)
+    _floats(d, dw_post, dw_pre)
     if dgate is not None:
         _floats(0 if gate is None else gate.numel(), dgate)
-    b = _norm_block(dr, y, dn, w_post, gate, w_pre, dr.dtype, gate_group, res_scale, block_scale,
-                    0.0)
-    _call_on(device, "norm_residual_backward", stream, ctypes.byref(b), _ptr(dn), _ptr(dr_out),
-             _ptr(y), _ptr(r_out), _ptr(rstd_post), _ptr(rstd_pre), _ptr(dy), _ptr(dr),
-             _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), _ptr(ws), ws.numel() * ws.element_size())
+    b = _norm_block(T, d, _dtype_of(y), dr.dtype, _dtype_of(dn), (w_post, gate, w_pre),
+                    (wpost, gp, wpre), gate_group, res_scale, block_scale, 0.0)
+    _call_on(index, "norm_residual_backward", stream, ctypes.byref(b), dnp, drop, yp, rop, pp, qp,
+             dyp, drp, dwpost, dgp, dwpre, wsp, ws.numel() * ws.element_size())
 
 
 ADAMW_BLOCK = 256  # elements that share one scale of an 8-bit moment
@@ -502,7 +526,10 @@ class AdamWTensors:
         self._keep = []
         for c, t in zip(self._c, tensors):
             self._pack(c, t)
-        self.device = _same_device([x for t, _ in self._keep for x in t]) if self._keep else None
+        self.device = None
+        if self._keep:
+            index, _ = _addresses(*[x for t, _ in self._keep for x in t])
+            self.device = torch.device("cuda", index)
         self._args = TwAdamwArgsC()
 
     def _pack(self, c, t):
@@ -559,7 +586,7 @@ def adamw_step(tensors: AdamWTensors, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, s
     a = tensors._args
     a.lr, a.beta1, a.beta2, a.eps, a.step = lr, beta1, beta2, eps, step
     a.lr_dev, a.step_dev, a.grad_scale = _ptr(lr_dev), _ptr(step_dev), _ptr(grad_scale)
-    _call_on(tensors.device, "adamw_step", stream, tensors._c, tensors.count, ctypes.byref(a))
+    _call_on(tensors.device.index, "adamw_step", stream, tensors._c, tensors.count, ctypes.byref(a))
 
 
 def status_bits(dev_status) -> list:

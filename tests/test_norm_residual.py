@@ -148,9 +148,14 @@ def test_binding_refuses_host_tensors_and_mixed_weights():
     with pytest.raises(ValueError):
         twell.norm_residual_forward(x, x, None, None, x[0], x, x)
     with pytest.raises(TypeError):
-        twell._norm_block(x, x, x, torch.zeros(8), None, torch.zeros(8, dtype=BF), F32, 0, 1., 1., 0.)
+        twell._norm_block(4, 8, F32, F32, F32, (torch.zeros(8), None, torch.zeros(8, dtype=BF)),
+                          (None, None, None), 0, 1.0, 1.0, 0.0)
     with pytest.raises(ValueError):
-        twell._norm_block(x, x, x, None, torch.zeros(3, 8), None, F32, 2, 1.0, 1.0, 0.0)
+        twell._norm_block(4, 8, F32, F32, F32, (None, torch.zeros(3, 8), None), (None, None, None),
+                          2, 1.0, 1.0, 0.0)
+    with pytest.raises(TypeError):
+        twell._norm_block(4, 8, torch.float16, F32, F32, (None, None, None), (None, None, None), 0,
+                          1.0, 1.0, 0.0)
 
 
 # ------------------------------------------------------------------ GPU -----
