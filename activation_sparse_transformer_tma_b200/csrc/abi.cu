@@ -313,6 +313,79 @@ tw_status twell_ffn_small_batch(const void* x, const void* Wg_t, const void* Wu_
                                           y_dtype, ws, dev_status, stream));
 }
 
+static size_t gated_part(int32_t T, int32_t F) {
+  return ((size_t)T * (size_t)F * 2 + 255) & ~size_t(255);
+}
+
+size_t gated_ffn_workspace_size(int32_t T, int32_t d, int32_t F) {
+  if (T < 0 || d <= 0 || F <= 0) return 0;
+  return gated_part(T, F);
+}
+
+size_t gated_ffn_backward_workspace_size(int32_t T, int32_t d, int32_t F) {
+  if (T < 0 || d <= 0 || F <= 0) return 0;
+  return 3 * gated_part(T, F);
+}
+
+static tw_status check_gated(int32_t T, int32_t d, int32_t F, tw_act act) {
+  if (T < 0 || d <= 0 || F <= 0 || (int)act < TW_ACT_RELU || (int)act > TW_ACT_GELU_TANH)
+    return TW_ERR_INVALID_ARG;
+  if (d % 8 != 0 || F % 8 != 0 || d < 64 || F < 64) return TW_ERR_UNSUPPORTED;
+  return TW_OK;
+}
+
+tw_status gated_ffn_forward(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
+                            int32_t T, int32_t d, int32_t F, tw_act act, void* z_save,
+                            void* u_save, void* y, tw_dtype y_dtype, void* ws, size_t ws_bytes,
+                            int32_t* dev_status, cudaStream_t stream) {
+  tw_status st = check_gated(T, d, F, act);
+  if (st != TW_OK) return st;
+  if ((T > 0 && (!x || !y || !ws)) || !Wg_t || !Wu_t || !Wd || !dtype_ok(y_dtype) ||
+      (z_save != nullptr) != (u_save != nullptr))
+    return TW_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, Wg_t, Wu_t, Wd, z_save, u_save, y, ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return TW_ERR_ALIGNMENT;
+  if (T == 0) return TW_OK;
+  if (ws_bytes < gated_ffn_workspace_size(T, d, F)) return TW_ERR_WORKSPACE;
+  return from_cuda(tw::launch_gated_forward(x, Wg_t, Wu_t, Wd, T, d, F, act,
+                                            static_cast<uint16_t*>(ws),
+                                            static_cast<uint16_t*>(z_save),
+                                            static_cast<uint16_t*>(u_save), y, y_dtype, dev_status,
+                                            stream));
+}
+
+tw_status gated_ffn_backward(const void* x, const void* dy, const void* Wg_t, const void* Wu_t,
+                             const void* Wd, int32_t T, int32_t d, int32_t F, tw_act act,
+                             const void* z_save, const void* u_save, void* dx, tw_dtype dx_dtype,
+                             void* dWg_t, void* dWu_t, void* dWd, tw_dtype dw_dtype, void* ws,
+                             size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  tw_status st = check_gated(T, d, F, act);
+  if (st != TW_OK) return st;
+  if ((T > 0 && (!x || !dy || !z_save || !u_save || !dx || !ws)) || !Wg_t || !Wu_t || !Wd ||
+      !dWg_t || !dWu_t || !dWd || !dtype_ok(dx_dtype) || !dtype_ok(dw_dtype))
+    return TW_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, dy, Wg_t, Wu_t, Wd, z_save, u_save, dx, dWg_t, dWu_t, dWd, ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return TW_ERR_ALIGNMENT;
+  if (T == 0) {  // no tokens: zero weight gradients
+    const size_t bytes = (dw_dtype == TW_BF16 ? 2 : 4) * (size_t)F * d;
+    void* grads[] = {dWg_t, dWu_t, dWd};
+    for (void* g : grads) {
+      cudaError_t e = cudaMemsetAsync(g, 0, bytes, stream);
+      if (e != cudaSuccess) return from_cuda(e);
+    }
+    return TW_OK;
+  }
+  if (ws_bytes < gated_ffn_backward_workspace_size(T, d, F)) return TW_ERR_WORKSPACE;
+  uint16_t* base = static_cast<uint16_t*>(ws);
+  const size_t part = gated_part(T, F) / 2;
+  return from_cuda(tw::launch_gated_backward(
+      x, dy, Wg_t, Wu_t, Wd, T, d, F, act, static_cast<const uint16_t*>(z_save),
+      static_cast<const uint16_t*>(u_save), base, base + part, base + 2 * part, dx, dx_dtype, dWg_t,
+      dWu_t, dWd, dw_dtype, dev_status, stream));
+}
+
 static tw_status check_norm_block(const tw_norm_block* b, bool has_y) {
   if (!b) return TW_ERR_INVALID_ARG;
   if (b->T < 0 || b->d <= 0 || !dtype_ok(b->y_dtype) || !dtype_ok(b->r_dtype) ||

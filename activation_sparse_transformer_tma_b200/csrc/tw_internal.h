@@ -131,6 +131,19 @@ cudaError_t launch_hybrid_backward(const void* x, const void* dy, const tw_hybri
                                    float* dWu_t, float* dWd, void* ws, size_t ws_bytes,
                                    int32_t* status, cudaStream_t stream);
 
+// Dense gated FFN with a choice of activation (gated_ffn.cu).  Arguments validated by
+// the caller; h, du, dz [T][F] bf16 scratch.
+cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
+                                 int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z,
+                                 uint16_t* u, void* y, tw_dtype y_dtype, int32_t* status,
+                                 cudaStream_t stream);
+cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_t, const void* Wu_t,
+                                  const void* Wd, int T, int d, int F, tw_act act,
+                                  const uint16_t* z, const uint16_t* u, uint16_t* h, uint16_t* du,
+                                  uint16_t* dz, void* dx, tw_dtype dx_dtype, void* dWg_t,
+                                  void* dWu_t, void* dWd, tw_dtype dw_dtype, int32_t* status,
+                                  cudaStream_t stream);
+
 // Norms around a block (norm_residual.cu).  Arguments validated by the caller.
 constexpr int kNormMaxD = 8192;
 cudaError_t launch_norm_forward(const tw_norm_block& b, const void* y, const void* r, void* r_out,

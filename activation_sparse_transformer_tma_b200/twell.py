@@ -29,6 +29,8 @@ EXPORTS = ["twell_gate_gemm", "twell_fused_updown_workspace_size", "twell_fused_
            "hybrid_ffn_backward_workspace_size", "hybrid_ffn_backward", "dense_ffn_forward",
            "dense_ffn_train_workspace_size", "dense_ffn_train_saved_bytes",
            "dense_ffn_train_forward", "dense_ffn_train_backward",
+           "gated_ffn_workspace_size", "gated_ffn_forward",
+           "gated_ffn_backward_workspace_size", "gated_ffn_backward",
            "norm_residual_forward", "norm_residual_backward_workspace_size",
            "norm_residual_backward", "adamw_step",
            "tw_test_withhold_next_gate_loads", "tw_measure_row_gather", "tw_measure_stream_read", "tw_status_string",
@@ -127,6 +129,14 @@ def lib():
                                               vp, vp, vp]
         L.dense_ffn_train_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, ctypes.c_float,
                                                vp, ctypes.c_size_t, vp, vp, vp, vp, vp, vp]
+        sz, ci = ctypes.c_size_t, ctypes.c_int
+        for name in ("gated_ffn_workspace_size", "gated_ffn_backward_workspace_size"):
+            getattr(L, name).argtypes = [i32, i32, i32]
+            getattr(L, name).restype = sz
+        L.gated_ffn_forward.argtypes = [vp, vp, vp, vp, i32, i32, i32, ci, vp, vp, vp, ci, vp, sz,
+                                        vp, vp]
+        L.gated_ffn_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, ci, vp, vp, vp, ci, vp,
+                                         vp, vp, ci, vp, sz, vp, vp]
         PN = ctypes.POINTER(TwNormBlockC)
         L.norm_residual_forward.argtypes = [PN, vp, vp, vp, vp, vp, vp, vp]
         L.norm_residual_backward_workspace_size.argtypes = [i32, i32, i32]
@@ -149,7 +159,8 @@ def lib():
                      "twell_to_hybrid",
                      "hybrid_ffn_forward", "hybrid_ffn_backward", "dense_ffn_forward",
                      "dense_ffn_train_forward", "dense_ffn_train_backward",
-                     "norm_residual_forward", "norm_residual_backward", "adamw_step"):
+                     "gated_ffn_forward", "gated_ffn_backward", "norm_residual_forward",
+                     "norm_residual_backward", "adamw_step"):
             getattr(L, name).restype = st
         _lib = L
     return _lib
@@ -413,6 +424,84 @@ def dense_train_saved(ws, T, F):
     """Views of the g, u, h [T][F] bf16 tensors the training forward saved in ws."""
     part = (T * F * 2 + 255) // 256 * 256
     return [ws[i * part:i * part + T * F * 2].view(torch.bfloat16).view(T, F) for i in range(3)]
+
+
+ACTIVATIONS = {"relu": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def _all_bf16(*tensors):
+    for t in tensors:
+        if t is not None and t.dtype != torch.bfloat16:
+            raise TypeError(f"bf16 expected, got {t.dtype}")
+
+
+def _dtype_code(t):
+    try:
+        return _DTYPE_CODES[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {t.dtype}") from None
+
+
+def _check_ffn(x, Wg_t, Wu_t, Wd):
+    T, d = x.shape
+    F = Wg_t.shape[0]
+    for w in (Wg_t, Wu_t, Wd):
+        if w.shape != (F, d):
+            raise ValueError(f"weights of {tuple(w.shape)} and {(F, d)} for rows of {d}")
+    _all_bf16(x, Wg_t, Wu_t, Wd)
+    return T, d, F
+
+
+def gated_ffn_workspace_size(T, d, F):
+    return int(lib().gated_ffn_workspace_size(T, d, F))
+
+
+def gated_ffn_backward_workspace_size(T, d, F):
+    return int(lib().gated_ffn_backward_workspace_size(T, d, F))
+
+
+def gated_ffn_workspace(T, d, F, training=False, device="cuda"):
+    """A caller-owned workspace tensor for gated_ffn_forward, and with `training`
+    for gated_ffn_backward too."""
+    with torch.cuda.device(device):
+        size = gated_ffn_workspace_size(T, d, F)
+        if training:
+            size = max(size, gated_ffn_backward_workspace_size(T, d, F))
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def gated_ffn_forward(x, Wg_t, Wu_t, Wd, act, y, ws, z=None, u=None, dev_status=None, stream=None):
+    """y = (act(x Wg) * (x Wu)) Wd for x [T, d] and weights [F, d], all bf16; act is a key of
+    ACTIVATIONS, y bf16 or fp32.  z and u [T, F] bf16 keep what gated_ffn_backward needs."""
+    index, (xp, gp, up, dp, yp, wsp, zp, usp, sp) = _addresses(x, Wg_t, Wu_t, Wd, y, ws, z, u,
+                                                               dev_status)
+    T, d, F = _check_ffn(x, Wg_t, Wu_t, Wd)
+    _all_bf16(z, u)
+    _same_shape(x, y)
+    for t in (z, u):
+        if t is not None and t.shape != (T, F):
+            raise ValueError(f"z and u of {(T, F)} expected, got {tuple(t.shape)}")
+    _call_on(index, "gated_ffn_forward", stream, xp, gp, up, dp, T, d, F, ACTIVATIONS[act], zp, usp,
+             yp, _dtype_code(y), wsp, ws.numel() * ws.element_size(), sp)
+
+
+def gated_ffn_backward(x, dy, Wg_t, Wu_t, Wd, act, z, u, dx, dWg_t, dWu_t, dWd, ws,
+                       dev_status=None, stream=None):
+    """Gradients of gated_ffn_forward: dx [T, d] and dWg_t, dWu_t, dWd [F, d], bf16 or fp32, from
+    dy [T, d] bf16 and the saved z and u."""
+    index, (xp, dyp, gp, up, dp, zp, usp, dxp, dgp, dup, ddp, wsp, sp) = _addresses(
+        x, dy, Wg_t, Wu_t, Wd, z, u, dx, dWg_t, dWu_t, dWd, ws, dev_status)
+    T, d, F = _check_ffn(x, Wg_t, Wu_t, Wd)
+    _all_bf16(dy, z, u)
+    _same_shape(x, dy, dx)
+    _same_shape(Wg_t, dWg_t, dWu_t, dWd)
+    if z.shape != (T, F) or u.shape != (T, F):
+        raise ValueError(f"z and u of {(T, F)} expected")
+    if dWg_t.dtype != dWu_t.dtype or dWg_t.dtype != dWd.dtype:
+        raise TypeError("the weight gradients differ in dtype")
+    _call_on(index, "gated_ffn_backward", stream, xp, dyp, gp, up, dp, T, d, F, ACTIVATIONS[act],
+             zp, usp, dxp, _dtype_code(dx), dgp, dup, ddp, _dtype_code(dWg_t), wsp,
+             ws.numel() * ws.element_size(), sp)
 
 
 def _norm_block(T, d, y_dtype, r_dtype, n_dtype, weights, addresses, gate_group, res_scale,

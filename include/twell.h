@@ -71,6 +71,11 @@ typedef enum {
 
 typedef enum { TW_F32 = 0, TW_BF16 = 1 } tw_dtype;
 
+/* Activations of the gated FFN: max(z, 0), z / (1 + exp(-z)), z Phi(z) with the
+ * normal distribution function Phi, and z / (1 + exp(-2k)) = z (1 + tanh k) / 2 with
+ * k = sqrt(2/pi) (z + 0.044715 z^3). */
+typedef enum { TW_ACT_RELU = 0, TW_ACT_SILU = 1, TW_ACT_GELU = 2, TW_ACT_GELU_TANH = 3 } tw_act;
+
 /*
  * TwELL tensor for the gate activations g [T][F] (section 2.1): the F columns
  * are cut into K = F / W tiles of width W.  For every (tile k, token t):
@@ -315,6 +320,43 @@ TW_API tw_status dense_ffn_train_backward(const void* x, const void* dy, const v
                                           int32_t F, float l1_lambda, void* ws, size_t ws_bytes,
                                           float* dx, float* dWg_t, float* dWu_t, float* dWd,
                                           int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Dense gated FFN with a choice of activation, for layers whose gate is not sparse;
+ * bf16 only, on the tcgen05 tensor cores with CTA pairs, weights laid out as on the
+ * sparse path (Wg_t, Wu_t, Wd all [F][d]):
+ *   z = x Wg, u = x Wu, h = act(z) u, y = h Wd (y_dtype).
+ * z and u are accumulated in fp32 and h = act(z) u is rounded once to bf16, the
+ * down projection's operand.  z_save and u_save [T][F] bf16 receive z and u for the
+ * backward; both NULL for inference.
+ * Limits: d % 8 == 0, F % 8 == 0, d >= 64, F >= 64, T >= 0 (with T == 0 the arrays
+ * sized by T may be NULL).
+ * ws: at least gated_ffn_workspace_size(T, d, F) bytes, asked with the device
+ * current that runs the call; calls sharing one workspace must not overlap on the device.
+ */
+TW_API size_t gated_ffn_workspace_size(int32_t T, int32_t d, int32_t F);
+TW_API tw_status gated_ffn_forward(const void* x, const void* Wg_t, const void* Wu_t,
+                                   const void* Wd, int32_t T, int32_t d, int32_t F, tw_act act,
+                                   void* z_save, void* u_save, void* y, tw_dtype y_dtype, void* ws,
+                                   size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Gradients of gated_ffn_forward for the loss sum(y * dy), from the saved z and u:
+ *   dh = dy Wd^T, du = dh act(z), dz = dh u act'(z),
+ *   dx = du Wu^T + dz Wg^T (dx_dtype),
+ *   dWd = h^T dy, dWu_t = du^T x, dWg_t = dz^T x ([F][d], dw_dtype, overwritten).
+ * dy [T][d] bf16.  h (from the saved z and u), du and dz are rounded to bf16 as the
+ * operands of the products; sums are fp32, in a fixed order.  act'(0) = 0 for ReLU.
+ * ws: at least gated_ffn_backward_workspace_size(T, d, F) bytes (h, du, dz).  With
+ * T == 0 the weight gradients are zeroed.
+ */
+TW_API size_t gated_ffn_backward_workspace_size(int32_t T, int32_t d, int32_t F);
+TW_API tw_status gated_ffn_backward(const void* x, const void* dy, const void* Wg_t,
+                                    const void* Wu_t, const void* Wd, int32_t T, int32_t d,
+                                    int32_t F, tw_act act, const void* z_save, const void* u_save,
+                                    void* dx, tw_dtype dx_dtype, void* dWg_t, void* dWu_t,
+                                    void* dWd, tw_dtype dw_dtype, void* ws, size_t ws_bytes,
+                                    int32_t* dev_status, cudaStream_t stream);
 
 /*
  * The norms before and after a block (for instance the FFN), fused with the

@@ -1,4 +1,4 @@
-"""fp64 numpy oracle of the operators around the FFN: the norms before and after a
+"""fp64 numpy oracle of the dense gated FFN and what stands around an FFN: the norms before and after a
 block with its gate and residual sum, and AdamW with fp32 or 8-bit
 moments.  Test infrastructure only; written from the formulas."""
 import numpy as np
@@ -95,3 +95,34 @@ def norm_backward(dn, dr_out, y, r_out, w_post, gate, w_pre, p, q, *, gate_group
         out["dgate"] = np.zeros_like(gate)
         np.add.at(out["dgate"], row, s * G * o)
     return out
+
+
+def activation(name, z):
+    """act(z) and act'(z)."""
+    from scipy.special import expit, ndtr
+    if name == "relu":
+        return np.maximum(z, 0.0), (z > 0).astype(np.float64)
+    if name == "silu":
+        p = expit(z)
+        return z * p, p * (1 + z * (1 - p))
+    if name == "gelu":
+        return z * ndtr(z), ndtr(z) + z * np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+    c = np.sqrt(2 / np.pi)
+    t = np.tanh(c * (z + 0.044715 * z ** 3))
+    return 0.5 * z * (1 + t), 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * c * (1 + 3 * 0.044715 * z * z)
+
+
+def gated_ffn(x, Wg, Wu, Wd, act):
+    """z, u, h, y of the dense gated FFN; weights [F, d]."""
+    z, u = x @ Wg.T, x @ Wu.T
+    h = activation(act, z)[0] * u
+    return z, u, h, h @ Wd
+
+
+def gated_ffn_backward(x, dy, Wg, Wu, Wd, act, z, u):
+    """Gradients from z and u: dict of h, dh, du, dz, dx, dWg, dWu, dWd."""
+    a, da = activation(act, z)
+    h, dh = a * u, dy @ Wd.T
+    du, dz = dh * a, dh * u * da
+    return dict(h=h, dh=dh, du=du, dz=dz, dx=du @ Wu + dz @ Wg, dWg=dz.T @ x, dWu=du.T @ x,
+                dWd=h.T @ dy)
