@@ -34,25 +34,38 @@ namespace {
 constexpr int kBM = 128;  // rows of A (and of B) a CTA
 constexpr int kBN = 256;  // columns of a tile
 constexpr int kBK = 64;   // 64 bf16 = one 128-byte swizzle row
-constexpr int kStages = 6;
 constexpr int kHalfBytes = kBM * kBK * 2;       // one operand's share of a stage
 constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kTmemCols = 2 * kBN;
 
+// Staging of the elementwise epilogues: a warp's 32 rows x 32 columns of up to three
+// bf16 matrices, in two turns, moved by TMA (64-byte swizzle).
+constexpr int kSlabBytes = 32 * 32 * 2;
+constexpr int kTurnBytes = 3 * kSlabBytes;
+constexpr int kStagingBytes = kEpiWarps * 2 * kTurnBytes;
+
 struct Tail {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
+  uint64_t full[6];
+  uint64_t empty[6];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
+  uint64_t loaded[kEpiWarps][2];
   uint32_t tmem_base;
   int abort;
   int never;
 };
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + sizeof(Tail);
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
+// Six stages of the operands' ring, or four beside the staging.
+template <class Epi>
+struct Layout {
+  static constexpr int kStages = Epi::kStaged ? 4 : 6;
+  static constexpr size_t kRing = (size_t)kStages * kStageBytes;
+  static constexpr size_t kStaging = Epi::kStaged ? kStagingBytes : 0;
+  static constexpr size_t kSmem = 1024 + kRing + kStaging + sizeof(Tail);
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
 
 // ------------------------------------------------------------- pair helpers --
 TW_DEV uint32_t pair_rank() {
@@ -152,6 +165,94 @@ TW_DEV void activate(float z, float& a, float& da) {
   }
 }
 
+// ----------------------------------------------------------------- staging --
+TW_DEV void tma_load_own(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+TW_DEV void tma_store(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1) : "memory");
+}
+TW_DEV void stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int PENDING>
+TW_DEV void stores_read() {  // all but the newest PENDING groups have read their slabs
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
+}
+TW_DEV void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+TW_DEV void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// A lane's row of a slab: 16-byte chunk q (8 columns) in its swizzled place.
+TW_DEV uint32_t slab_chunk(uint32_t slab, int lane, int q) {
+  return slab + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+}
+TW_DEV void slab_write(uint32_t slab, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(slab_chunk(slab, lane, q)), "r"(w[4 * q]), "r"(w[4 * q + 1]),
+                   "r"(w[4 * q + 2]), "r"(w[4 * q + 3]) : "memory");
+}
+TW_DEV void slab_read(uint32_t slab, int lane, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[4 * q]), "=r"(w[4 * q + 1]), "=r"(w[4 * q + 2]), "=r"(w[4 * q + 3])
+                 : "r"(slab_chunk(slab, lane, q)) : "memory");
+}
+
+struct Maps {
+  CUtensorMap a[3], b[3];
+  CUtensorMap e[5];  // of the epilogue, boxes of 32 columns x 32 rows
+};
+
+// ------------------------------------------------------------------- tiles --
+// One launch's tiles.  Order: groups of kGroupM tile rows, within a group down the
+// rows first, so the pairs at work share few rows of A and few of B in L2.  When the
+// last round of tiles would leave half of the pairs idle, its tiles are cut into
+// two of 128 columns (`full` tiles before them; MN-major B only).
+constexpr int kGroupM = 8;
+struct Tile {
+  int product, m, col, width;  // tile row; first column (of units: dual B), columns
+};
+struct Tiles {
+  int m, n, products, kblocks, full, count;
+  TW_DEV Tile at(int i, int n_step) const {
+    Tile t;
+    int tile = i, part = 0;
+    t.width = kBN;
+    if (i >= full) {
+      tile = full + ((i - full) >> 1);
+      part = (i - full) & 1;
+      t.width = kBN / 2;
+    }
+    t.product = tile / (m * n);
+    const int k = tile - t.product * (m * n);
+    const int group = k / (kGroupM * n), in = k - group * (kGroupM * n);
+    const int rows = m - group * kGroupM < kGroupM ? m - group * kGroupM : kGroupM;
+    const int tn = in / rows;
+    t.m = group * kGroupM + in - tn * rows;
+    t.col = tn * n_step + part * (kBN / 2);
+    return t;
+  }
+};
+
+// What an epilogue warp works with.
+struct EpiWarp {
+  int warp, lane, q, half, rank;  // index among the epilogue warps; lane quarter; column half
+  int pair, pairs;
+  uint32_t slabs;     // its staging
+  uint64_t* loaded;   // its two barriers of staged loads
+  volatile int* abort;
+  uint64_t timeout_ns;
+  TW_DEV int row0(const Tile& t) const { return t.m * 2 * kBM + rank * kBM + q * 32; }
+  TW_DEV uint32_t slab(int turn, int which) const {
+    return slabs + turn * kTurnBytes + which * kSlabBytes;
+  }
+};
+
 // ---------------------------------------------------------------- epilogues --
 // Operand layout of a product:
 //   kDualB  B is gate (first CTA) beside up (second CTA), 128 units each
@@ -159,98 +260,149 @@ TW_DEV void activate(float z, float& a, float& da) {
 //   kBMN    B is MN-major: B[n][k] read from a [K][N] row-major tensor
 //   kDualK  the reduction runs over (a[0], b[0]) and then (a[1], b[1])
 //   kGroup  independent products of one shape, (a[p], b[p]) -> out[p]
-template <bool DUALB, bool AMN, bool BMN, bool DUALK, bool GROUP>
+//   kStaged the epilogue goes through staging slabs
+// begin() comes before the first tile, run() once a tile (false: a wait ran out),
+// end() after the last.
+template <bool DUALB, bool AMN, bool BMN, bool DUALK, bool GROUP, bool STAGED>
 struct Operands {
-  static constexpr bool kDualB = DUALB, kAMN = AMN, kBMN = BMN, kDualK = DUALK, kGroup = GROUP;
+  static constexpr bool kDualB = DUALB, kAMN = AMN, kBMN = BMN, kDualK = DUALK, kGroup = GROUP,
+                        kStaged = STAGED;
+  static constexpr int kStep = DUALB ? 128 : kBN;  // output columns a tile
 };
-
-// 32 bf16 columns of one row, stored 8 at a time as far as they exist.
-TW_DEV void store_bf16(uint16_t* dst, const uint32_t (&w)[16], int left) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (left > 8 * q)
-      reinterpret_cast<uint4*>(dst)[q] =
-          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-}
-TW_DEV void load_bf16(const uint16_t* src, uint32_t (&w)[16], int left) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (left > 8 * q) v = reinterpret_cast<const uint4*>(src)[q];
-    w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
-  }
-}
 
 // h = act(z) u from the unrounded z and u; z and u are kept (bf16) for the backward
 // where it asks for them.
-struct EpiGateUp : Operands<true, false, false, false, false> {
+struct EpiGateUp : Operands<true, false, false, false, false, true> {
   int T, F, act;
-  uint16_t *h, *z, *u;
+  bool keep;
+  // maps.e: h, z, u
+  struct State {
+    int turn;
+  };
+  TW_DEV void begin(State& s, const EpiWarp&, const Maps&, const Tiles&) const { s.turn = 0; }
   template <int ACT>
-  TW_DEV void rows(uint32_t taddr, int row, int tile_n, int half) const {
+  TW_DEV void rows(State& s, const EpiWarp& w, const Maps& maps, uint32_t taddr,
+                   const Tile& t) const {
+    const int row0 = w.row0(t);
+    if (row0 >= T) return;  // uniform over the warp, as all conditions below
 #pragma unroll 1
-    for (int c = half * 64; c < half * 64 + 64; c += 32) {
-      const int col = tile_n * 128 + c;
-      if (col >= F) break;  // uniform
-      uint32_t zr[32], ur[32];
+    for (int c = w.half * 64; c < w.half * 64 + 64; c += 32) {
+      const int col = t.col + c;
+      if (col >= F) break;
+      uint32_t zr[32], ur[32], out[16];
       __syncwarp();
       tmem_ld_32x32b_x32(taddr + c, zr);
       tmem_ld_32x32b_x32(taddr + 128 + c, ur);
+      // the stores of this turn's last use have read its slabs
+      if (w.lane == 0) stores_read<1>();
+      __syncwarp();
       tmem_ld_wait();
-      if (row >= T) continue;
-      const size_t off = (size_t)row * F + col;
-      uint32_t w[16];
-      if (z) {
+      if (keep) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          w[i] = pack_bf16x2(__uint_as_float(zr[2 * i]), __uint_as_float(zr[2 * i + 1]));
-        store_bf16(z + off, w, F - col);
+          out[i] = pack_bf16x2(__uint_as_float(zr[2 * i]), __uint_as_float(zr[2 * i + 1]));
+        slab_write(w.slab(s.turn, 1), w.lane, out);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          w[i] = pack_bf16x2(__uint_as_float(ur[2 * i]), __uint_as_float(ur[2 * i + 1]));
-        store_bf16(u + off, w, F - col);
+          out[i] = pack_bf16x2(__uint_as_float(ur[2 * i]), __uint_as_float(ur[2 * i + 1]));
+        slab_write(w.slab(s.turn, 2), w.lane, out);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float a0, a1, da;
         activate<ACT>(__uint_as_float(zr[2 * i]), a0, da);
         activate<ACT>(__uint_as_float(zr[2 * i + 1]), a1, da);
-        w[i] = pack_bf16x2(a0 * __uint_as_float(ur[2 * i]), a1 * __uint_as_float(ur[2 * i + 1]));
+        out[i] = pack_bf16x2(a0 * __uint_as_float(ur[2 * i]), a1 * __uint_as_float(ur[2 * i + 1]));
       }
-      store_bf16(h + off, w, F - col);
+      slab_write(w.slab(s.turn, 0), w.lane, out);
+      fence_async_proxy();
+      __syncwarp();
+      if (w.lane == 0) {  // rows and columns past the end are not stored
+        tma_store(&maps.e[0], w.slab(s.turn, 0), col, row0);
+        if (keep) {
+          tma_store(&maps.e[1], w.slab(s.turn, 1), col, row0);
+          tma_store(&maps.e[2], w.slab(s.turn, 2), col, row0);
+        }
+        stores_commit();
+      }
+      s.turn ^= 1;
     }
   }
-  TW_DEV void run(uint32_t taddr, int row, int tile_n, int half, int) const {
+  TW_DEV bool run(State& s, const EpiWarp& w, const Maps& maps, const Tiles&, uint32_t taddr,
+                  const Tile& t) const {
     switch (act) {
-      case TW_ACT_RELU: rows<TW_ACT_RELU>(taddr, row, tile_n, half); break;
-      case TW_ACT_SILU: rows<TW_ACT_SILU>(taddr, row, tile_n, half); break;
-      case TW_ACT_GELU: rows<TW_ACT_GELU>(taddr, row, tile_n, half); break;
-      default: rows<TW_ACT_GELU_TANH>(taddr, row, tile_n, half); break;
+      case TW_ACT_RELU: rows<TW_ACT_RELU>(s, w, maps, taddr, t); break;
+      case TW_ACT_SILU: rows<TW_ACT_SILU>(s, w, maps, taddr, t); break;
+      case TW_ACT_GELU: rows<TW_ACT_GELU>(s, w, maps, taddr, t); break;
+      default: rows<TW_ACT_GELU_TANH>(s, w, maps, taddr, t); break;
     }
+    return true;
+  }
+  TW_DEV void end(State&, const EpiWarp& w) const {
+    if (w.lane == 0) stores_done();
   }
 };
 
 // From dh and the kept z and u: h again (bf16, the operand of dWd: keeping z and u
 // alone holds a third less between the passes), du = dh act(z), dz = dh u act'(z).
-struct EpiBackward : Operands<false, false, false, false, false> {
+// z and u of the next 32 columns are loaded while these are worked on; du and dz are
+// written over the z and u they came from.
+struct EpiBackward : Operands<false, false, false, false, false, true> {
   int T, F, act;
-  const uint16_t *z, *u;
-  uint16_t *h, *du, *dz;
+  // maps.e: h, z, u, du, dz
+  struct State {
+    uint32_t chunk;          // chunks worked on: turn chunk & 1, its barrier's phase (chunk >> 1) & 1
+    int next_tile, next_c;   // the chunk to load next (next_tile >= count: none)
+    uint32_t ahead;          // chunks loaded
+  };
+  // Moves the cursor to the first chunk at or behind it that has rows and columns.
+  TW_DEV void seek(State& s, const EpiWarp& w, const Tiles& tiles) const {
+    for (; s.next_tile < tiles.count; s.next_tile += w.pairs, s.next_c = 0) {
+      const Tile t = tiles.at(s.next_tile, kStep);
+      if (s.next_c < 128 && w.row0(t) < T && t.col + w.half * 128 + s.next_c < F) return;
+    }
+  }
+  TW_DEV void load_next(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles) const {
+    if (s.next_tile >= tiles.count) return;
+    if (w.lane == 0) {
+      const Tile t = tiles.at(s.next_tile, kStep);
+      const int turn = s.ahead & 1, col = t.col + w.half * 128 + s.next_c;
+      stores_read<0>();  // the slabs' last stores have been read
+      mbar_arrive_expect_tx(&w.loaded[turn], 2 * kSlabBytes);
+      tma_load_own(w.slab(turn, 1), &maps.e[1], &w.loaded[turn], col, w.row0(t));
+      tma_load_own(w.slab(turn, 2), &maps.e[2], &w.loaded[turn], col, w.row0(t));
+    }
+    ++s.ahead;
+    s.next_c += 32;
+    seek(s, w, tiles);
+  }
+  TW_DEV void begin(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles) const {
+    s.chunk = s.ahead = 0;
+    s.next_tile = w.pair;
+    s.next_c = 0;
+    seek(s, w, tiles);
+    load_next(s, w, maps, tiles);
+  }
   template <int ACT>
-  TW_DEV void rows(uint32_t taddr, int row, int tile_n, int half) const {
+  TW_DEV bool rows(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles,
+                   uint32_t taddr, const Tile& t) const {
+    const int row0 = w.row0(t);
+    if (row0 >= T) return true;  // uniform over the warp, as all conditions below
 #pragma unroll 1
-    for (int c = half * 128; c < half * 128 + 128; c += 32) {
-      const int col = tile_n * kBN + c;
-      if (col >= F) break;  // uniform
-      uint32_t r[32];
+    for (int c = w.half * 128; c < w.half * 128 + 128; c += 32) {
+      const int col = t.col + c;
+      if (col >= F) break;
+      const int turn = s.chunk & 1;
+      load_next(s, w, maps, tiles);
+      uint32_t r[32], zw[16], uw[16], hw[16];
       __syncwarp();
       tmem_ld_32x32b_x32(taddr + c, r);
+      bool ok = mbar_wait(&w.loaded[turn], (s.chunk >> 1) & 1u, w.abort, w.timeout_ns);
+      ok = __all_sync(0xFFFFFFFFu, ok);
       tmem_ld_wait();
-      if (row >= T) continue;
-      const size_t off = (size_t)row * F + col;
-      uint32_t zw[16], uw[16], hw[16];
-      load_bf16(z + off, zw, F - col);
-      load_bf16(u + off, uw, F - col);
+      if (!ok) return false;
+      slab_read(w.slab(turn, 1), w.lane, zw);
+      slab_read(w.slab(turn, 2), w.lane, uw);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float dh0 = __uint_as_float(r[2 * i]), dh1 = __uint_as_float(r[2 * i + 1]);
@@ -262,31 +414,59 @@ struct EpiBackward : Operands<false, false, false, false, false> {
         uw[i] = pack_bf16x2(dh0 * a0, dh1 * a1);
         zw[i] = pack_bf16x2(dh0 * u0 * d0, dh1 * u1 * d1);
       }
-      store_bf16(h + off, hw, F - col);
-      store_bf16(du + off, uw, F - col);
-      store_bf16(dz + off, zw, F - col);
+      slab_write(w.slab(turn, 0), w.lane, hw);
+      slab_write(w.slab(turn, 1), w.lane, zw);
+      slab_write(w.slab(turn, 2), w.lane, uw);
+      fence_async_proxy();
+      __syncwarp();
+      if (w.lane == 0) {
+        tma_store(&maps.e[0], w.slab(turn, 0), col, row0);
+        tma_store(&maps.e[4], w.slab(turn, 1), col, row0);
+        tma_store(&maps.e[3], w.slab(turn, 2), col, row0);
+        stores_commit();
+      }
+      ++s.chunk;
+    }
+    return true;
+  }
+  TW_DEV bool run(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles, uint32_t taddr,
+                  const Tile& t) const {
+    switch (act) {
+      case TW_ACT_RELU: return rows<TW_ACT_RELU>(s, w, maps, tiles, taddr, t);
+      case TW_ACT_SILU: return rows<TW_ACT_SILU>(s, w, maps, tiles, taddr, t);
+      case TW_ACT_GELU: return rows<TW_ACT_GELU>(s, w, maps, tiles, taddr, t);
+      default: return rows<TW_ACT_GELU_TANH>(s, w, maps, tiles, taddr, t);
     }
   }
-  TW_DEV void run(uint32_t taddr, int row, int tile_n, int half, int) const {
-    switch (act) {
-      case TW_ACT_RELU: rows<TW_ACT_RELU>(taddr, row, tile_n, half); break;
-      case TW_ACT_SILU: rows<TW_ACT_SILU>(taddr, row, tile_n, half); break;
-      case TW_ACT_GELU: rows<TW_ACT_GELU>(taddr, row, tile_n, half); break;
-      default: rows<TW_ACT_GELU_TANH>(taddr, row, tile_n, half); break;
-    }
+  TW_DEV void end(State&, const EpiWarp& w) const {
+    if (w.lane == 0) stores_done();
   }
 };
 
-// Plain results [M][N], rounded once to bf16 or stored in fp32.
+// 32 bf16 columns of one row, stored 8 at a time as far as they exist.
+TW_DEV void store_bf16(uint16_t* dst, const uint32_t (&w)[16], int left) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (left > 8 * q)
+      reinterpret_cast<uint4*>(dst)[q] =
+          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+}
+
+// Plain results [M][N], rounded once to bf16 or stored in fp32.  Long reductions
+// leave time for plain stores.
 template <class Ops>
 struct EpiStore : Ops {
   int M, N;
   bool bf16;
   void* out[3];
-  TW_DEV void run(uint32_t taddr, int row, int tile_n, int half, int product) const {
+  struct State {};
+  TW_DEV void begin(State&, const EpiWarp&, const Maps&, const Tiles&) const {}
+  TW_DEV bool run(State&, const EpiWarp& w, const Maps&, const Tiles&, uint32_t taddr,
+                  const Tile& t) const {
+    const int row = w.row0(t) + w.lane, part = t.width / 2;
 #pragma unroll 1
-    for (int c = half * 128; c < half * 128 + 128; c += 32) {
-      const int col = tile_n * kBN + c;
+    for (int c = w.half * part; c < w.half * part + part; c += 32) {
+      const int col = t.col + c;
       if (col >= N) break;  // uniform
       uint32_t r[32];
       __syncwarp();
@@ -295,13 +475,13 @@ struct EpiStore : Ops {
       if (row >= M) continue;
       const size_t off = (size_t)row * N + col;
       if (bf16) {
-        uint32_t w[16];
+        uint32_t v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        store_bf16(static_cast<uint16_t*>(out[product]) + off, w, N - col);
+          v[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        store_bf16(static_cast<uint16_t*>(out[t.product]) + off, v, N - col);
       } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out[product]) + off);
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out[t.product]) + off);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (N - col > 4 * q)
@@ -309,45 +489,29 @@ struct EpiStore : Ops {
                                  __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
       }
     }
+    return true;
   }
+  TW_DEV void end(State&, const EpiWarp&) const {}
 };
-using OpsDown = Operands<false, false, true, false, false>;
-using OpsDx = Operands<false, false, true, true, false>;
-using OpsGrads = Operands<false, true, true, false, true>;
-
-struct Maps {
-  CUtensorMap a[3], b[3];
-};
-
-// Tiles of one launch.  Order: groups of kGroupM tile rows, within a group down
-// the rows first, so the pairs at work share few rows of A and few of B in L2.
-constexpr int kGroupM = 8;
-struct Tiles {
-  int m, n, products, kblocks;
-  TW_DEV int count() const { return m * n * products; }
-  TW_DEV void at(int tile, int& product, int& tm, int& tn) const {
-    product = tile / (m * n);
-    const int t = tile - product * (m * n);
-    const int group = t / (kGroupM * n), in = t - group * (kGroupM * n);
-    const int rows = m - group * kGroupM < kGroupM ? m - group * kGroupM : kGroupM;
-    tn = in / rows;
-    tm = group * kGroupM + in - tn * rows;
-  }
-};
+using OpsDown = Operands<false, false, true, false, false, false>;
+using OpsDx = Operands<false, false, true, true, false, false>;
+using OpsGrads = Operands<false, true, true, false, true, false>;
 
 // ------------------------------------------------------------------- kernel --
 template <class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_gemm_kernel(const __grid_constant__ Maps maps, const Tiles tiles, const Epi epi,
                      int32_t* status, unsigned long long timeout_ns) {
+  constexpr int kStages = Layout<Epi>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  auto* sm = reinterpret_cast<Tail*>(smem + (size_t)kStages * kStageBytes);
+  uint8_t* staging = smem + Layout<Epi>::kRing;
+  auto* sm = reinterpret_cast<Tail*>(staging + Layout<Epi>::kStaging);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)pair_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int count = tiles.count(), kblocks = tiles.kblocks;
+  const int count = tiles.count, kblocks = tiles.kblocks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -359,6 +523,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&sm->tmem_empty[a], 2 * kEpiWarps);
     }
     mbar_init(&sm->drain, 1);
+    for (int w = 0; w < kEpiWarps; ++w) {
+      mbar_init(&sm->loaded[w][0], 1);
+      mbar_init(&sm->loaded[w][1], 1);
+    }
     sm->abort = 0;
     sm->never = 0;
     fence_mbar_init();
@@ -382,11 +550,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int tile = pair; tile < count && ok; tile += pairs) {
-        int product, tm, tn;
-        tiles.at(tile, product, tm, tn);
-        const int m0 = tm * 2 * kBM + rank * kBM;
+        const Tile t = tiles.at(tile, Epi::kStep);
+        const int m0 = t.m * 2 * kBM + rank * kBM;
         // dual B: this CTA's weight, 128 units; otherwise its half of the columns
-        const int n0 = Epi::kDualB ? tn * 128 : tn * kBN + rank * 128;
+        const int n0 = Epi::kDualB ? t.col : t.col + rank * (t.width / 2);
+        const bool narrow = Epi::kBMN && t.width < kBN;
+        const uint32_t bytes = 2 * (kHalfBytes + (narrow ? kHalfBytes / 2 : kHalfBytes));
         for (int kb = 0; kb < kblocks; ++kb) {
           const uint32_t s = it % kStages;
           if (!mbar_wait(&sm->empty[s], ((it / kStages) & 1u) ^ 1u, abort, timeout_ns)) {
@@ -396,12 +565,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint8_t* a = smem + (size_t)s * kStageBytes;
           uint8_t* b = a + kHalfBytes;
           const uint32_t bar = leader_addr(&sm->full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&sm->full[s], 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(&sm->full[s], bytes);
           const bool second = Epi::kDualK && kb >= kblocks / 2;
           const int k0 = (second ? kb - kblocks / 2 : kb) * kBK;
-          const CUtensorMap* ma = &maps.a[Epi::kGroup ? product : second ? 1 : 0];
+          const CUtensorMap* ma = &maps.a[Epi::kGroup ? t.product : second ? 1 : 0];
           const CUtensorMap* mb =
-              &maps.b[Epi::kGroup ? product : Epi::kDualB ? rank : second ? 1 : 0];
+              &maps.b[Epi::kGroup ? t.product : Epi::kDualB ? rank : second ? 1 : 0];
           if (Epi::kAMN) {  // boxes of 64 k-rows x 64 columns
             tma_load_pair(a, ma, bar, m0, k0);
             tma_load_pair(a + kHalfBytes / 2, ma, bar, m0 + 64, k0);
@@ -410,7 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (Epi::kBMN) {
             tma_load_pair(b, mb, bar, n0, k0);
-            tma_load_pair(b + kHalfBytes / 2, mb, bar, n0 + 64, k0);
+            if (!narrow) tma_load_pair(b + kHalfBytes / 2, mb, bar, n0 + 64, k0);
           } else {
             tma_load_pair(b, mb, bar, k0, n0);
           }
@@ -429,7 +598,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // -------------------------------------------------------- MMA issuer --
-      constexpr uint32_t idesc = idesc_bf16_f32(2 * kBM, kBN, Epi::kAMN, Epi::kBMN);
       uint32_t it = 0, tl = 0;
       bool ok = true;
       for (int tile = pair; tile < count && ok; tile += pairs, ++tl) {
@@ -440,6 +608,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * kBN;
+        const uint32_t idesc = tile < tiles.full
+                                   ? idesc_bf16_f32(2 * kBM, kBN, Epi::kAMN, Epi::kBMN)
+                                   : idesc_bf16_f32(2 * kBM, kBN / 2, Epi::kAMN, Epi::kBMN);
         for (int kb = 0; kb < kblocks; ++kb) {
           const uint32_t s = it % kStages;
           if (!mbar_wait(&sm->full[s], (it / kStages) & 1u, abort, timeout_ns)) {
@@ -474,27 +645,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- epilogue -----
-    const int q = warp & 3;           // TMEM lane quarter this warp may access
-    const int half = (warp - 2) >> 2;  // of the tile's columns
+    EpiWarp w;
+    w.warp = warp - 2;
+    w.lane = lane;
+    w.q = warp & 3;  // TMEM lane quarter this warp may access
+    w.half = w.warp >> 2;
+    w.rank = rank;
+    w.pair = pair;
+    w.pairs = pairs;
+    w.slabs = smem_u32(staging) + w.warp * 2 * kTurnBytes;
+    w.loaded = sm->loaded[w.warp];
+    w.abort = abort;
+    w.timeout_ns = timeout_ns;
+    typename Epi::State state;
+    epi.begin(state, w, maps, tiles);
     uint32_t tl = 0;
     for (int tile = pair; tile < count; tile += pairs, ++tl) {
-      int product, tm, tn;
-      tiles.at(tile, product, tm, tn);
+      const Tile t = tiles.at(tile, Epi::kStep);
       const uint32_t acc = tl & 1u;
       bool ok = mbar_wait(&sm->tmem_full[acc], (tl >> 1) & 1u, abort, timeout_ns);
       ok = __all_sync(0xFFFFFFFFu, ok);
+      if (ok) {
+        tc_fence_after();
+        ok = epi.run(state, w, maps, tiles,
+                     tmem_base + ((uint32_t)(w.q * 32) << 16) + acc * kBN, t);
+      }
       if (!ok) {
         *abort = 1;
-        if (lane == 0) set_status(status, kStatusTimeout);
+        if (lane == 0) {
+          set_status(status, kStatusTimeout);
+          const uint64_t t0 = globaltimer_ns();  // as in the producer
+          while (globaltimer_ns() - t0 < 1000000u) {}
+        }
         break;
       }
-      tc_fence_after();
-      const int row = tm * 2 * kBM + rank * kBM + q * 32 + lane;
-      epi.run(tmem_base + ((uint32_t)(q * 32) << 16) + acc * kBN, row, tn, half, product);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(leader_addr(&sm->tmem_empty[acc]));
     }
+    epi.end(state, w);
   }
   tc_fence_before();
   __syncwarp();
@@ -509,17 +698,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // --------------------------------------------------------------------- host --
 template <class Epi>
-cudaError_t launch_pairs(const Maps& maps, const Tiles& t, const Epi& epi, int32_t* status,
-                         cudaStream_t stream) {
-  const long long count = (long long)t.m * t.n * t.products;
+cudaError_t launch_pairs(const Maps& maps, int m, int n, int products, int kblocks, const Epi& epi,
+                         int32_t* status, cudaStream_t stream) {
+  const long long count = (long long)m * n * products;
   if (count == 0) return cudaSuccess;
   if (count > 0x3FFFFFFF) return cudaErrorInvalidValue;
-  cudaError_t e =
-      set_smem_limit(reinterpret_cast<const void*>(pair_gemm_kernel<Epi>), (int)kSmem);
+  constexpr size_t smem = Layout<Epi>::kSmem;
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(pair_gemm_kernel<Epi>), (int)smem);
   if (e != cudaSuccess) return e;
-  const int most = num_sms() / 2;
-  const int pairs = count < most ? (int)count : most;
-  return launch_pdl(pair_gemm_kernel<Epi>, dim3(2 * pairs), dim3(kThreads), kSmem, stream, maps, t,
+  const int most = num_sms() / 2 > 0 ? num_sms() / 2 : 1;
+  Tiles t{m, n, products, kblocks, (int)count, (int)count};
+  const int rest = (int)(count % most);
+  if (Epi::kBMN && rest > 0 && 2 * rest <= most) {
+    t.full = (int)count - rest;
+    t.count = t.full + 2 * rest;
+  }
+  const int pairs = t.count < most ? t.count : most;
+  return launch_pdl(pair_gemm_kernel<Epi>, dim3(2 * pairs), dim3(kThreads), smem, stream, maps, t,
                     epi, status, kWaitTimeoutNs);
 }
 
@@ -532,6 +727,11 @@ bool map_mn(CUtensorMap* m, const void* base, uint64_t k_rows, uint64_t cols) {
   return make_tmap_bf16(m, base, k_rows, cols, 64, kBK);
 }
 
+// A matrix of the staged epilogues: 32 x 32 boxes.
+bool map_slab(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
+  return make_tmap_bf16_sw64(m, base, rows, cols, 32);
+}
+
 int div_up(int a, int b) { return a / b + (a % b != 0); }
 
 }  // namespace
@@ -542,24 +742,24 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
                                  cudaStream_t stream) {
   Maps m1{}, m2{};
   if (!map_k(&m1.a[0], x, T, d) || !map_k(&m1.b[0], Wg_t, F, d) || !map_k(&m1.b[1], Wu_t, F, d) ||
-      !map_k(&m2.a[0], h, T, F) || !map_mn(&m2.b[0], Wd, F, d))
+      !map_slab(&m1.e[0], h, T, F) || (z && !map_slab(&m1.e[1], z, T, F)) ||
+      (z && !map_slab(&m1.e[2], u, T, F)) || !map_k(&m2.a[0], h, T, F) ||
+      !map_mn(&m2.b[0], Wd, F, d))
     return cudaErrorInvalidValue;
   EpiGateUp e1;
   e1.T = T;
   e1.F = F;
   e1.act = act;
-  e1.h = h;
-  e1.z = z;
-  e1.u = u;
+  e1.keep = z != nullptr;
   const int mt = div_up(T, 2 * kBM);
-  cudaError_t e = launch_pairs(m1, Tiles{mt, div_up(F, 128), 1, div_up(d, kBK)}, e1, status, stream);
+  cudaError_t e = launch_pairs(m1, mt, div_up(F, 128), 1, div_up(d, kBK), e1, status, stream);
   if (e != cudaSuccess) return e;
   EpiStore<OpsDown> e2;
   e2.M = T;
   e2.N = d;
   e2.bf16 = y_dtype == TW_BF16;
   e2.out[0] = e2.out[1] = e2.out[2] = y;
-  return launch_pairs(m2, Tiles{mt, div_up(d, kBN), 1, div_up(F, kBK)}, e2, status, stream);
+  return launch_pairs(m2, mt, div_up(d, kBN), 1, div_up(F, kBK), e2, status, stream);
 }
 
 cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_t, const void* Wu_t,
@@ -573,27 +773,24 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
       !map_k(&m2.a[1], dz, T, F) || !map_mn(&m2.b[0], Wu_t, F, d) ||
       !map_mn(&m2.b[1], Wg_t, F, d) || !map_mn(&m3.a[0], h, T, F) || !map_mn(&m3.a[1], du, T, F) ||
       !map_mn(&m3.a[2], dz, T, F) || !map_mn(&m3.b[0], dy, T, d) || !map_mn(&m3.b[1], x, T, d) ||
-      !map_mn(&m3.b[2], x, T, d))
+      !map_mn(&m3.b[2], x, T, d) || !map_slab(&m1.e[0], h, T, F) || !map_slab(&m1.e[1], z, T, F) ||
+      !map_slab(&m1.e[2], u, T, F) || !map_slab(&m1.e[3], du, T, F) ||
+      !map_slab(&m1.e[4], dz, T, F))
     return cudaErrorInvalidValue;
   EpiBackward e1;
   e1.T = T;
   e1.F = F;
   e1.act = act;
-  e1.z = z;
-  e1.u = u;
-  e1.h = h;
-  e1.du = du;
-  e1.dz = dz;
   const int mt = div_up(T, 2 * kBM), nd = div_up(d, kBN);
   cudaError_t e =
-      launch_pairs(m1, Tiles{mt, div_up(F, kBN), 1, div_up(d, kBK)}, e1, status, stream);
+      launch_pairs(m1, mt, div_up(F, kBN), 1, div_up(d, kBK), e1, status, stream);
   if (e != cudaSuccess) return e;
   EpiStore<OpsDx> e2;
   e2.M = T;
   e2.N = d;
   e2.bf16 = dx_dtype == TW_BF16;
   e2.out[0] = e2.out[1] = e2.out[2] = dx;
-  e = launch_pairs(m2, Tiles{mt, nd, 1, 2 * div_up(F, kBK)}, e2, status, stream);
+  e = launch_pairs(m2, mt, nd, 1, 2 * div_up(F, kBK), e2, status, stream);
   if (e != cudaSuccess) return e;
   EpiStore<OpsGrads> e3;
   e3.M = F;
@@ -602,7 +799,7 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
   e3.out[0] = dWd;
   e3.out[1] = dWu_t;
   e3.out[2] = dWg_t;
-  return launch_pairs(m3, Tiles{div_up(F, 2 * kBM), nd, 3, div_up(T, kBK)}, e3, status, stream);
+  return launch_pairs(m3, div_up(F, 2 * kBM), nd, 3, div_up(T, kBK), e3, status, stream);
 }
 
 }  // namespace tw

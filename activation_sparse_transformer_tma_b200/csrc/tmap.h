@@ -12,4 +12,9 @@ namespace tw {
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                     uint32_t box_cols, uint32_t box_rows);
 
+// The same with 64-byte swizzling: boxes of 32 columns, 16-byte chunk c of row r of
+// the box at chunk c ^ ((r >> 1) & 3) of its 64 bytes.
+bool make_tmap_bf16_sw64(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                         uint32_t box_rows);
+
 }  // namespace tw
