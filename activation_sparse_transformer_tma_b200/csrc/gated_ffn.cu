@@ -25,6 +25,8 @@
 // pair at the last barrier.
 #include "tmap.h"
 #include "pdl.cuh"
+#include "cluster.cuh"
+#include "gated_act.cuh"
 #include "tw_common.cuh"
 #include "tw_internal.h"
 
@@ -68,19 +70,9 @@ struct Layout {
 };
 
 // ------------------------------------------------------------- pair helpers --
-TW_DEV uint32_t pair_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-TW_DEV void pair_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
 // Address of `bar` in the first CTA of the pair.
 TW_DEV uint32_t leader_addr(const uint64_t* bar) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
-  return r;
+  return place_in(smem_u32(bar), 0);
 }
 // Load into this CTA's shared memory; the bytes are counted on the leader's barrier.
 TW_DEV void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t leader_bar, int c0, int c1) {
@@ -136,32 +128,6 @@ TW_DEV bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort, uint6
       if (t0 == 0) t0 = now;
       else if (now - t0 > timeout_ns) return false;
     }
-  }
-}
-
-// -------------------------------------------------------------- activations --
-// act(z) and act'(z).  exp and the division are the approximate instructions: the
-// results are rounded to bf16.
-template <int ACT>
-TW_DEV void activate(float z, float& a, float& da) {
-  if (ACT == TW_ACT_RELU) {
-    a = z > 0.f ? z : 0.f;
-    da = z > 0.f ? 1.f : 0.f;
-    if (z != z) a = da = z;
-  } else if (ACT == TW_ACT_SILU) {
-    const float p = __fdividef(1.f, 1.f + __expf(-z));
-    a = z * p;
-    da = p * fmaf(z, 1.f - p, 1.f);
-  } else if (ACT == TW_ACT_GELU) {
-    const float cdf = 0.5f * (1.f + erff(z * 0.70710678f));
-    a = z * cdf;
-    da = fmaf(z * 0.39894228f, __expf(-0.5f * z * z), cdf);
-  } else {
-    // 0.5 (1 + tanh(k)) = 1 / (1 + exp(-2k)) =: p, k = sqrt(2/pi) (z + 0.044715 z^3)
-    const float p =
-        __fdividef(1.f, 1.f + __expf(-1.5957691f * z * fmaf(0.044715f * z, z, 1.f)));
-    a = z * p;
-    da = fmaf(z * p * (1.f - p), 1.5957691f * fmaf(0.134145f * z, z, 1.f), p);
   }
 }
 
@@ -509,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* staging = smem + Layout<Epi>::kRing;
   auto* sm = reinterpret_cast<Tail*>(staging + Layout<Epi>::kStaging);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)pair_rank();
+  const int rank = (int)cta_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int count = tiles.count, kblocks = tiles.kblocks;
 
@@ -537,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  pair_sync();
+  cluster_meet();
   tc_fence_after();
   const uint32_t tmem_base = sm->tmem_base;
   volatile int* abort = &sm->abort;
@@ -688,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncwarp();
   __syncthreads();
-  pair_sync();  // no CTA leaves while the other may still arrive on its barriers
+  cluster_meet();  // no CTA leaves while the other may still arrive on its barriers
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -740,6 +706,8 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
                                  int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z,
                                  uint16_t* u, void* y, tw_dtype y_dtype, int32_t* status,
                                  cudaStream_t stream) {
+  if (T <= kGatedFewMaxT)
+    return launch_gated_few(x, Wg_t, Wu_t, Wd, T, d, F, act, h, z, u, y, y_dtype, status, stream);
   Maps m1{}, m2{};
   if (!map_k(&m1.a[0], x, T, d) || !map_k(&m1.b[0], Wg_t, F, d) || !map_k(&m1.b[1], Wu_t, F, d) ||
       !map_slab(&m1.e[0], h, T, F) || (z && !map_slab(&m1.e[1], z, T, F)) ||

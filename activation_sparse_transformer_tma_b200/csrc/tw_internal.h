@@ -137,6 +137,11 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
                                  int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z,
                                  uint16_t* u, void* y, tw_dtype y_dtype, int32_t* status,
                                  cudaStream_t stream);
+// The same forward for few tokens (gated_few.cu).
+constexpr int kGatedFewMaxT = 256;
+cudaError_t launch_gated_few(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
+                             int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z, uint16_t* u,
+                             void* y, tw_dtype y_dtype, int32_t* status, cudaStream_t stream);
 cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_t, const void* Wu_t,
                                   const void* Wd, int T, int d, int F, tw_act act,
                                   const uint16_t* z, const uint16_t* u, uint16_t* h, uint16_t* du,
