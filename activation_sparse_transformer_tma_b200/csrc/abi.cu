@@ -319,12 +319,12 @@ static size_t gated_part(int32_t T, int32_t F) {
 
 size_t gated_ffn_workspace_size(int32_t T, int32_t d, int32_t F) {
   if (T < 0 || d <= 0 || F <= 0) return 0;
-  return gated_part(T, F);
+  return gated_part(T, F) + tw::gated_forward_split_bytes(T, d, F);
 }
 
 size_t gated_ffn_backward_workspace_size(int32_t T, int32_t d, int32_t F) {
   if (T < 0 || d <= 0 || F <= 0) return 0;
-  return 3 * gated_part(T, F);
+  return 3 * gated_part(T, F) + tw::gated_backward_split_bytes(T, d, F);
 }
 
 static tw_status check_gated(int32_t T, int32_t d, int32_t F, tw_act act) {
@@ -351,7 +351,8 @@ tw_status gated_ffn_forward(const void* x, const void* Wg_t, const void* Wu_t, c
   return from_cuda(tw::launch_gated_forward(x, Wg_t, Wu_t, Wd, T, d, F, act,
                                             static_cast<uint16_t*>(ws),
                                             static_cast<uint16_t*>(z_save),
-                                            static_cast<uint16_t*>(u_save), y, y_dtype, dev_status,
+                                            static_cast<uint16_t*>(u_save), y, y_dtype,
+                                            static_cast<char*>(ws) + gated_part(T, F), dev_status,
                                             stream));
 }
 
@@ -383,7 +384,7 @@ tw_status gated_ffn_backward(const void* x, const void* dy, const void* Wg_t, co
   return from_cuda(tw::launch_gated_backward(
       x, dy, Wg_t, Wu_t, Wd, T, d, F, act, static_cast<const uint16_t*>(z_save),
       static_cast<const uint16_t*>(u_save), base, base + part, base + 2 * part, dx, dx_dtype, dWg_t,
-      dWu_t, dWd, dw_dtype, dev_status, stream));
+      dWu_t, dWd, dw_dtype, base + 3 * part, dev_status, stream));
 }
 
 static tw_status check_norm_block(const tw_norm_block* b, bool has_y) {

@@ -14,7 +14,7 @@
 // so the result does not depend on timing.  The exchange takes the ring's place.
 //
 // The second kernel is launched while the first runs (programmatic dependent
-// launch) and both fit on one SM up to 64 tokens.  It starts to read Wd at once -- the
+// launch).  It starts to read Wd at once -- the
 // first kernel has waited for whatever came before it, and does not write Wd -- and
 // waits for the first kernel before it reads h.
 //
@@ -214,15 +214,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 2 && !*abort) {
     const int row = (warp & 3) * 32 + lane;
     const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    // column by column to the CTA that finishes the token
+    const uint32_t mine = exchange + ((rank * part * kRows + row) << 2);
+    int to = 0, at = 0;
+    uint32_t place = place_in(mine, 0);
     for (int c = 0; c < f.N; c += 16) {
       uint32_t r[16];
       tmem_ld_x16(taddr + c, r);
       tmem_ld_wait();
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const int to = (c + k) / part, at = (c + k) - to * part;
-        store_in(place_in(exchange + (((rank * part + at) * kRows + row) << 2), to),
-                 __uint_as_float(r[k]));
+        store_in(place + at * (kRows * 4), __uint_as_float(r[k]));
+        if (++at == part) {
+          at = 0;
+          if (++to < ranks) place = place_in(mine, to);
+        }
       }
     }
     tc_fence_before();
@@ -272,10 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Cluster size: CTAs for every SM, as far as whole k-blocks go round.
+// Cluster size: up to two CTAs for every SM, as far as whole k-blocks go round.
 int cluster_of(int tiles, int kblocks) {
   int s = 1;
-  while (s < kMaxCluster && 2 * s * tiles <= num_sms() && 2 * s <= kblocks) s *= 2;
+  while (s < kMaxCluster && 2 * s * tiles <= 2 * num_sms() && 2 * s <= kblocks) s *= 2;
   return s;
 }
 
@@ -284,9 +290,12 @@ cudaError_t launch_few(const CUtensorMap& w0, const CUtensorMap& w1, const CUten
                        Few f, int tiles, int32_t* status, cudaStream_t stream) {
   f.N = (f.T + 15) / 16 * 16;
   f.stage_bytes = kWBytes + f.N * kBK * 2;
-  // both kernels on one SM up to 64 tokens; beyond, the whole SM for deeper rings
-  const int room = f.N <= 64 ? 106 * 1024 : 220 * 1024;
+  // two CTAs on an SM, of one kernel or of both (deeper rings, an SM each, were slower)
+  const int room = 106 * 1024;
   f.stages = room / f.stage_bytes < kMaxStages ? room / f.stage_bytes : kMaxStages;
+  static_assert(kRows * kGatedFewMaxT * 4 <= 106 / (16 + kGatedFewMaxT / 8) *
+                                                 (16 + kGatedFewMaxT / 8) * 1024,
+                "the exchange fits the ring of the most tokens");
   f.tmem_cols = 32;
   while ((int)f.tmem_cols < f.N) f.tmem_cols *= 2;
   const size_t smem = 1024 + (size_t)f.stages * f.stage_bytes + sizeof(Tail);

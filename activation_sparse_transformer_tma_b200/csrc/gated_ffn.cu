@@ -178,15 +178,21 @@ struct Maps {
 // One launch's tiles.  Order: groups of kGroupM tile rows, within a group down the
 // rows first, so the pairs at work share few rows of A and few of B in L2.  When the
 // last round of tiles would leave half of the pairs idle, its tiles are cut into
-// two of 128 columns (`full` tiles before them; MN-major B only).
+// two of 128 columns (`full` tiles before them; MN-major B only).  A launch of few
+// tiles, all of them cut so, also divides the reduction into `splits`.
 constexpr int kGroupM = 8;
 struct Tile {
   int product, m, col, width;  // tile row; first column (of units: dual B), columns
+  int k0, k1;                  // k-blocks
 };
 struct Tiles {
-  int m, n, products, kblocks, full, count;
+  int m, n, products, kblocks, full, count, splits;
   TW_DEV Tile at(int i, int n_step) const {
     Tile t;
+    const int split = i % splits;
+    i /= splits;
+    t.k0 = split * kblocks / splits;
+    t.k1 = (split + 1) * kblocks / splits;
     int tile = i, part = 0;
     t.width = kBN;
     if (i >= full) {
@@ -236,16 +242,27 @@ struct Operands {
   static constexpr int kStep = DUALB ? 128 : kBN;  // output columns a tile
 };
 
+// Counters of the launch behind this one, cleared by one warp.
+TW_DEV void clear(const EpiWarp& w, uint32_t* words, int n) {
+  if (w.pair == 0 && w.rank == 0 && w.warp == 0)
+    for (int i = w.lane; i < n; i += 32) words[i] = 0u;
+}
+
 // h = act(z) u from the unrounded z and u; z and u are kept (bf16) for the backward
 // where it asks for them.
 struct EpiGateUp : Operands<true, false, false, false, false, true> {
   int T, F, act;
   bool keep;
+  uint32_t* arrived;  // the next product's arrival counters, cleared here
+  int n_arrived;
   // maps.e: h, z, u
   struct State {
     int turn;
   };
-  TW_DEV void begin(State& s, const EpiWarp&, const Maps&, const Tiles&) const { s.turn = 0; }
+  TW_DEV void begin(State& s, const EpiWarp& w, const Maps&, const Tiles&) const {
+    s.turn = 0;
+    clear(w, arrived, n_arrived);
+  }
   template <int ACT>
   TW_DEV void rows(State& s, const EpiWarp& w, const Maps& maps, uint32_t taddr,
                    const Tile& t) const {
@@ -295,7 +312,7 @@ struct EpiGateUp : Operands<true, false, false, false, false, true> {
     }
   }
   TW_DEV bool run(State& s, const EpiWarp& w, const Maps& maps, const Tiles&, uint32_t taddr,
-                  const Tile& t) const {
+                  const Tile& t, int) const {
     switch (act) {
       case TW_ACT_RELU: rows<TW_ACT_RELU>(s, w, maps, taddr, t); break;
       case TW_ACT_SILU: rows<TW_ACT_SILU>(s, w, maps, taddr, t); break;
@@ -315,6 +332,8 @@ struct EpiGateUp : Operands<true, false, false, false, false, true> {
 // written over the z and u they came from.
 struct EpiBackward : Operands<false, false, false, false, false, true> {
   int T, F, act;
+  uint32_t* arrived;  // as in EpiGateUp
+  int n_arrived;
   // maps.e: h, z, u, du, dz
   struct State {
     uint32_t chunk;          // chunks worked on: turn chunk & 1, its barrier's phase (chunk >> 1) & 1
@@ -343,6 +362,7 @@ struct EpiBackward : Operands<false, false, false, false, false, true> {
     seek(s, w, tiles);
   }
   TW_DEV void begin(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles) const {
+    clear(w, arrived, n_arrived);
     s.chunk = s.ahead = 0;
     s.next_tile = w.pair;
     s.next_c = 0;
@@ -396,7 +416,7 @@ struct EpiBackward : Operands<false, false, false, false, false, true> {
     return true;
   }
   TW_DEV bool run(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles, uint32_t taddr,
-                  const Tile& t) const {
+                  const Tile& t, int) const {
     switch (act) {
       case TW_ACT_RELU: return rows<TW_ACT_RELU>(s, w, maps, tiles, taddr, t);
       case TW_ACT_SILU: return rows<TW_ACT_SILU>(s, w, maps, tiles, taddr, t);
@@ -425,10 +445,84 @@ struct EpiStore : Ops {
   int M, N;
   bool bf16;
   void* out[3];
+  float* parts;      // partial sums and arrival counters of a divided reduction
+  uint32_t* arrived;
   struct State {};
   TW_DEV void begin(State&, const EpiWarp&, const Maps&, const Tiles&) const {}
-  TW_DEV bool run(State&, const EpiWarp& w, const Maps&, const Tiles&, uint32_t taddr,
-                  const Tile& t) const {
+  // 32 columns of this lane's row.
+  TW_DEV void store(const Tile& t, int row, int col, const uint32_t (&r)[32]) const {
+    if (row >= M) return;
+    const size_t off = (size_t)row * N + col;
+    if (bf16) {
+      uint32_t v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      store_bf16(static_cast<uint16_t*>(out[t.product]) + off, v, N - col);
+    } else {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out[t.product]) + off);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (N - col > 4 * q)
+          dst[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                               __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+    }
+  }
+  // A divided reduction (width 128: 64 columns a warp).  Every part writes its sums;
+  // the warp that arrives last at its place adds all parts in their order, so the
+  // result does not depend on which one that is, and no one waits.
+  TW_DEV void join(const EpiWarp& w, const Tiles& tiles, uint32_t taddr, const Tile& t,
+                   int index) const {
+    constexpr int kPlace = 2 * 8 * 32 * 4;  // floats of a warp's 32 x 64 sums
+    const int S = tiles.splits, unit = index / S, split = index - unit * S;
+    const int place = (unit * 2 + w.rank) * kEpiWarps + w.warp;
+    const int col0 = t.col + w.half * 64;
+    if (col0 >= N) return;  // uniform
+    float4* mine = reinterpret_cast<float4*>(parts + ((size_t)place * S + split) * kPlace) + w.lane;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(taddr + w.half * 64 + c * 32, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        mine[(c * 8 + q) * 32] =
+            make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                        __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+    }
+    __threadfence();
+    __syncwarp();
+    uint32_t before = 0;
+    if (w.lane == 0) before = atomicAdd(&arrived[place], 1u);
+    before = __shfl_sync(0xFFFFFFFFu, before, 0);
+    if ((int)before != S - 1) return;
+    __threadfence();
+    const float4* all = reinterpret_cast<const float4*>(parts + (size_t)place * S * kPlace) + w.lane;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      uint32_t r[32];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < S; ++k) {
+          const float4 o = __ldcg(all + (size_t)k * (kPlace / 4) + (c * 8 + q) * 32);
+          v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+        }
+        r[4 * q] = __float_as_uint(v.x);
+        r[4 * q + 1] = __float_as_uint(v.y);
+        r[4 * q + 2] = __float_as_uint(v.z);
+        r[4 * q + 3] = __float_as_uint(v.w);
+      }
+      if (col0 + c * 32 < N) store(t, w.row0(t) + w.lane, col0 + c * 32, r);
+    }
+  }
+  TW_DEV bool run(State&, const EpiWarp& w, const Maps&, const Tiles& tiles, uint32_t taddr,
+                  const Tile& t, int index) const {
+    if (tiles.splits > 1) {
+      join(w, tiles, taddr, t, index);
+      return true;
+    }
     const int row = w.row0(t) + w.lane, part = t.width / 2;
 #pragma unroll 1
     for (int c = w.half * part; c < w.half * part + part; c += 32) {
@@ -438,22 +532,7 @@ struct EpiStore : Ops {
       __syncwarp();
       tmem_ld_32x32b_x32(taddr + c, r);
       tmem_ld_wait();
-      if (row >= M) continue;
-      const size_t off = (size_t)row * N + col;
-      if (bf16) {
-        uint32_t v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          v[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        store_bf16(static_cast<uint16_t*>(out[t.product]) + off, v, N - col);
-      } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out[t.product]) + off);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (N - col > 4 * q)
-            dst[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                 __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
-      }
+      store(t, row, col, r);
     }
     return true;
   }
@@ -522,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int n0 = Epi::kDualB ? t.col : t.col + rank * (t.width / 2);
         const bool narrow = Epi::kBMN && t.width < kBN;
         const uint32_t bytes = 2 * (kHalfBytes + (narrow ? kHalfBytes / 2 : kHalfBytes));
-        for (int kb = 0; kb < kblocks; ++kb) {
+        for (int kb = t.k0; kb < t.k1; ++kb) {
           const uint32_t s = it % kStages;
           if (!mbar_wait(&sm->empty[s], ((it / kStages) & 1u) ^ 1u, abort, timeout_ns)) {
             ok = false;
@@ -574,10 +653,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * kBN;
-        const uint32_t idesc = tile < tiles.full
+        const Tile t = tiles.at(tile, Epi::kStep);
+        const uint32_t idesc = t.width == kBN
                                    ? idesc_bf16_f32(2 * kBM, kBN, Epi::kAMN, Epi::kBMN)
                                    : idesc_bf16_f32(2 * kBM, kBN / 2, Epi::kAMN, Epi::kBMN);
-        for (int kb = 0; kb < kblocks; ++kb) {
+        for (int kb = t.k0; kb < t.k1; ++kb) {
           const uint32_t s = it % kStages;
           if (!mbar_wait(&sm->full[s], (it / kStages) & 1u, abort, timeout_ns)) {
             ok = false;
@@ -593,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                           : sdesc_kmajor_sw128(a + kk * 32);
             const uint64_t bd = Epi::kBMN ? sdesc_mnmajor_sw128(b + kk * 2048, kBK * 64 * 2)
                                           : sdesc_kmajor_sw128(b + kk * 32);
-            umma_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+            umma_pair(d, ad, bd, idesc, kb != t.k0 || kk != 0 ? 1u : 0u);
           }
           umma_commit_pair(&sm->empty[s]);
           ++it;
@@ -634,7 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok) {
         tc_fence_after();
         ok = epi.run(state, w, maps, tiles,
-                     tmem_base + ((uint32_t)(w.q * 32) << 16) + acc * kBN, t);
+                     tmem_base + ((uint32_t)(w.q * 32) << 16) + acc * kBN, t, tile);
       }
       if (!ok) {
         *abort = 1;
@@ -663,23 +743,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------------- host --
-template <class Epi>
-cudaError_t launch_pairs(const Maps& maps, int m, int n, int products, int kblocks, const Epi& epi,
-                         int32_t* status, cudaStream_t stream) {
+int most_pairs() { return num_sms() / 2 > 0 ? num_sms() / 2 : 1; }
+
+constexpr int kMinSplitBlocks = 8;  // k-blocks of a part, at least
+constexpr int kMaxSplits = 8;
+
+// How a product's tiles are dealt out (narrow: with MN-major B).
+Tiles plan_tiles(int m, int n, int products, int kblocks, bool narrow) {
   const long long count = (long long)m * n * products;
-  if (count == 0) return cudaSuccess;
-  if (count > 0x3FFFFFFF) return cudaErrorInvalidValue;
+  Tiles t{m, n, products, kblocks, (int)count, (int)count, 1};
+  const int most = most_pairs(), rest = (int)(count % most);
+  if (narrow && rest > 0 && 2 * rest <= most) {
+    t.full = (int)count - rest;
+    t.count = t.full + 2 * rest;
+    if (t.full == 0) {
+      while (2 * t.splits <= kMaxSplits && 2 * t.splits * t.count <= most &&
+             kblocks / (2 * t.splits) >= kMinSplitBlocks)
+        t.splits *= 2;
+      t.count *= t.splits;
+    }
+  }
+  return t;
+}
+
+// Arrival counters and partial sums of a divided reduction, in bytes.
+int counters_of(const Tiles& t) { return t.splits > 1 ? t.count / t.splits * 2 * kEpiWarps : 0; }
+size_t counter_bytes(const Tiles& t) { return ((size_t)counters_of(t) * 4 + 255) & ~size_t(255); }
+size_t split_bytes(const Tiles& t) {
+  return t.splits > 1 ? counter_bytes(t) + (size_t)t.count * 2 * kBM * (kBN / 2) * 4 : 0;
+}
+
+template <class Epi>
+cudaError_t launch_pairs(const Maps& maps, const Tiles& t, const Epi& epi, int32_t* status,
+                         cudaStream_t stream) {
+  if (t.count == 0) return cudaSuccess;
   constexpr size_t smem = Layout<Epi>::kSmem;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(pair_gemm_kernel<Epi>), (int)smem);
   if (e != cudaSuccess) return e;
-  const int most = num_sms() / 2 > 0 ? num_sms() / 2 : 1;
-  Tiles t{m, n, products, kblocks, (int)count, (int)count};
-  const int rest = (int)(count % most);
-  if (Epi::kBMN && rest > 0 && 2 * rest <= most) {
-    t.full = (int)count - rest;
-    t.count = t.full + 2 * rest;
-  }
-  const int pairs = t.count < most ? t.count : most;
+  const int pairs = t.count < most_pairs() ? t.count : most_pairs();
   return launch_pdl(pair_gemm_kernel<Epi>, dim3(2 * pairs), dim3(kThreads), smem, stream, maps, t,
                     epi, status, kWaitTimeoutNs);
 }
@@ -702,10 +803,33 @@ int div_up(int a, int b) { return a / b + (a % b != 0); }
 
 }  // namespace
 
+namespace {
+Tiles down_tiles(int T, int d, int F) {
+  return plan_tiles(div_up(T, 2 * kBM), div_up(d, kBN), 1, div_up(F, kBK), true);
+}
+Tiles dx_tiles(int T, int d, int F) {
+  return plan_tiles(div_up(T, 2 * kBM), div_up(d, kBN), 1, 2 * div_up(F, kBK), true);
+}
+// The tiles' count of any product fits an int.
+bool too_large(int T, int d, int F) {
+  const long long mt = div_up(T, 2 * kBM), mf = div_up(F, 2 * kBM);
+  const long long nf = div_up(F, 128), nd = div_up(d, kBN);
+  return mt * nf > 0x3FFFFFFF || mt * nd > 0x3FFFFFFF || 3 * mf * nd > 0x3FFFFFFF;
+}
+}  // namespace
+
+size_t gated_forward_split_bytes(int T, int d, int F) {
+  return T <= kGatedFewMaxT || too_large(T, d, F) ? 0 : split_bytes(down_tiles(T, d, F));
+}
+size_t gated_backward_split_bytes(int T, int d, int F) {
+  return T == 0 || too_large(T, d, F) ? 0 : split_bytes(dx_tiles(T, d, F));
+}
+
 cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
                                  int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z,
-                                 uint16_t* u, void* y, tw_dtype y_dtype, int32_t* status,
-                                 cudaStream_t stream) {
+                                 uint16_t* u, void* y, tw_dtype y_dtype, void* split,
+                                 int32_t* status, cudaStream_t stream) {
+  if (too_large(T, d, F)) return cudaErrorInvalidValue;
   if (T <= kGatedFewMaxT)
     return launch_gated_few(x, Wg_t, Wu_t, Wd, T, d, F, act, h, z, u, y, y_dtype, status, stream);
   Maps m1{}, m2{};
@@ -719,23 +843,30 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
   e1.F = F;
   e1.act = act;
   e1.keep = z != nullptr;
-  const int mt = div_up(T, 2 * kBM);
-  cudaError_t e = launch_pairs(m1, mt, div_up(F, 128), 1, div_up(d, kBK), e1, status, stream);
+  const Tiles t2 = down_tiles(T, d, F);
+  e1.arrived = static_cast<uint32_t*>(split);
+  e1.n_arrived = counters_of(t2);
+  cudaError_t e = launch_pairs(
+      m1, plan_tiles(div_up(T, 2 * kBM), div_up(F, 128), 1, div_up(d, kBK), false), e1, status,
+      stream);
   if (e != cudaSuccess) return e;
   EpiStore<OpsDown> e2;
   e2.M = T;
   e2.N = d;
   e2.bf16 = y_dtype == TW_BF16;
   e2.out[0] = e2.out[1] = e2.out[2] = y;
-  return launch_pairs(m2, mt, div_up(d, kBN), 1, div_up(F, kBK), e2, status, stream);
+  e2.arrived = static_cast<uint32_t*>(split);
+  e2.parts = reinterpret_cast<float*>(static_cast<char*>(split) + counter_bytes(t2));
+  return launch_pairs(m2, t2, e2, status, stream);
 }
 
 cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_t, const void* Wu_t,
                                   const void* Wd, int T, int d, int F, tw_act act,
                                   const uint16_t* z, const uint16_t* u, uint16_t* h, uint16_t* du,
                                   uint16_t* dz, void* dx, tw_dtype dx_dtype, void* dWg_t,
-                                  void* dWu_t, void* dWd, tw_dtype dw_dtype, int32_t* status,
-                                  cudaStream_t stream) {
+                                  void* dWu_t, void* dWd, tw_dtype dw_dtype, void* split,
+                                  int32_t* status, cudaStream_t stream) {
+  if (too_large(T, d, F)) return cudaErrorInvalidValue;
   Maps m1{}, m2{}, m3{};
   if (!map_k(&m1.a[0], dy, T, d) || !map_k(&m1.b[0], Wd, F, d) || !map_k(&m2.a[0], du, T, F) ||
       !map_k(&m2.a[1], dz, T, F) || !map_mn(&m2.b[0], Wu_t, F, d) ||
@@ -749,16 +880,22 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
   e1.T = T;
   e1.F = F;
   e1.act = act;
-  const int mt = div_up(T, 2 * kBM), nd = div_up(d, kBN);
-  cudaError_t e =
-      launch_pairs(m1, mt, div_up(F, kBN), 1, div_up(d, kBK), e1, status, stream);
+  const Tiles t2 = dx_tiles(T, d, F);
+  e1.arrived = static_cast<uint32_t*>(split);
+  e1.n_arrived = counters_of(t2);
+  const int nd = div_up(d, kBN);
+  cudaError_t e = launch_pairs(
+      m1, plan_tiles(div_up(T, 2 * kBM), div_up(F, kBN), 1, div_up(d, kBK), false), e1, status,
+      stream);
   if (e != cudaSuccess) return e;
   EpiStore<OpsDx> e2;
   e2.M = T;
   e2.N = d;
   e2.bf16 = dx_dtype == TW_BF16;
   e2.out[0] = e2.out[1] = e2.out[2] = dx;
-  e = launch_pairs(m2, mt, nd, 1, 2 * div_up(F, kBK), e2, status, stream);
+  e2.arrived = static_cast<uint32_t*>(split);
+  e2.parts = reinterpret_cast<float*>(static_cast<char*>(split) + counter_bytes(t2));
+  e = launch_pairs(m2, t2, e2, status, stream);
   if (e != cudaSuccess) return e;
   EpiStore<OpsGrads> e3;
   e3.M = F;
@@ -767,7 +904,14 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
   e3.out[0] = dWd;
   e3.out[1] = dWu_t;
   e3.out[2] = dWg_t;
-  return launch_pairs(m3, div_up(F, 2 * kBM), nd, 3, div_up(T, kBK), e3, status, stream);
+  e3.arrived = nullptr;
+  e3.parts = nullptr;
+  Tiles t3 = plan_tiles(div_up(F, 2 * kBM), nd, 3, div_up(T, kBK), true);
+  if (t3.splits > 1) {  // small weights: no room is kept for their partial sums
+    t3.count /= t3.splits;
+    t3.splits = 1;
+  }
+  return launch_pairs(m3, t3, e3, status, stream);
 }
 
 }  // namespace tw

@@ -135,10 +135,13 @@ cudaError_t launch_hybrid_backward(const void* x, const void* dy, const tw_hybri
 // the caller; h, du, dz [T][F] bf16 scratch.
 cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
                                  int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z,
-                                 uint16_t* u, void* y, tw_dtype y_dtype, int32_t* status,
-                                 cudaStream_t stream);
+                                 uint16_t* u, void* y, tw_dtype y_dtype, void* split,
+                                 int32_t* status, cudaStream_t stream);
+// Workspace for dividing the reductions of y and dx (`split`), 0 where they are not.
+size_t gated_forward_split_bytes(int T, int d, int F);
+size_t gated_backward_split_bytes(int T, int d, int F);
 // The same forward for few tokens (gated_few.cu).
-constexpr int kGatedFewMaxT = 256;
+constexpr int kGatedFewMaxT = 128;
 cudaError_t launch_gated_few(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
                              int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z, uint16_t* u,
                              void* y, tw_dtype y_dtype, int32_t* status, cudaStream_t stream);
@@ -146,8 +149,8 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
                                   const void* Wd, int T, int d, int F, tw_act act,
                                   const uint16_t* z, const uint16_t* u, uint16_t* h, uint16_t* du,
                                   uint16_t* dz, void* dx, tw_dtype dx_dtype, void* dWg_t,
-                                  void* dWu_t, void* dWd, tw_dtype dw_dtype, int32_t* status,
-                                  cudaStream_t stream);
+                                  void* dWu_t, void* dWd, tw_dtype dw_dtype, void* split,
+                                  int32_t* status, cudaStream_t stream);
 
 // Norms around a block (norm_residual.cu).  Arguments validated by the caller.
 constexpr int kNormMaxD = 8192;

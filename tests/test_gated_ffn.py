@@ -169,7 +169,8 @@ def _check_forward(x, Wg, Wu, Wd, act, y, z=None, u=None):
 
 SHAPES = [(1, 64, 64), (2, 2048, 264), (3, 72, 200), (16, 128, 8192), (17, 520, 1024),
           (64, 256, 384), (65, 64, 136), (129, 128, 264), (256, 264, 128), (300, 1000, 520),
-          (513, 264, 1032), (1024, 512, 512), (8, 2048, 8192), (100, 1096, 2056)]
+          (513, 264, 1032), (1024, 512, 512), (8, 2048, 8192), (100, 1096, 2056), (200, 512, 2048),
+          (260, 264, 4104)]
 
 
 @pytest.mark.gpu
