@@ -4,6 +4,16 @@
 
 namespace tw {
 
+// True in one thread of a converged warp.  Unlike a test of the lane number it tells the
+// compiler that a single thread takes the branch: with the test of the lane, the four
+// MMAs of a 64-wide k-block took 637 cycles to issue, against 512 to execute.
+TW_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
 TW_DEV uint32_t cta_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

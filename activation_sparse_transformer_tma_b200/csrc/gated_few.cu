@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       auto stage = [&](int i) { return smem + (size_t)(i % f.stages) * f.stage_bytes; };
       auto weights = [&](int i) {
         uint8_t* a = stage(i);
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     pdl_wait();
     pdl_launch_next();
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = idesc_bf16_f32(kRows, f.N, DOWN, false);
       bool ok = true;
       for (int i = 0; i < n; ++i) {
