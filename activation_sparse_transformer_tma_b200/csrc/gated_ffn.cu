@@ -42,11 +42,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kTmemCols = 2 * kBN;
 
-// Staging of the elementwise epilogues: a warp's 32 rows x 32 columns of up to three
-// bf16 matrices, in two turns, moved by TMA (64-byte swizzle).
+// Staging of the elementwise epilogues: slabs of a warp's 32 rows x 32 columns of a
+// bf16 matrix, moved by TMA (64-byte swizzle).
 constexpr int kSlabBytes = 32 * 32 * 2;
-constexpr int kTurnBytes = 3 * kSlabBytes;
-constexpr int kStagingBytes = kEpiWarps * 2 * kTurnBytes;
 
 struct Tail {
   uint64_t full[6];
@@ -54,17 +52,16 @@ struct Tail {
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
-  uint64_t loaded[kEpiWarps][2];
+  uint64_t loaded[kEpiWarps];
   uint32_t tmem_base;
   int abort;
   int never;
 };
-// Six stages of the operands' ring, or four beside the staging.
+// Shared memory: the operands' ring, then each epilogue warp's slabs.
 template <class Epi>
 struct Layout {
-  static constexpr int kStages = Epi::kStaged ? 4 : 6;
-  static constexpr size_t kRing = (size_t)kStages * kStageBytes;
-  static constexpr size_t kStaging = Epi::kStaged ? kStagingBytes : 0;
+  static constexpr size_t kRing = (size_t)Epi::kStages * kStageBytes;
+  static constexpr size_t kStaging = (size_t)kEpiWarps * Epi::kSlabs * kSlabBytes;
   static constexpr size_t kSmem = 1024 + kRing + kStaging + sizeof(Tail);
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -154,6 +151,14 @@ TW_DEV void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" 
 TW_DEV uint32_t slab_chunk(uint32_t slab, int lane, int q) {
   return slab + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
 }
+// Chunks first and first + 1 of a lane's row: 16 columns.
+TW_DEV void slab_write16(uint32_t slab, int lane, int first, const uint32_t (&w)[8]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(slab_chunk(slab, lane, first + q)), "r"(w[4 * q]), "r"(w[4 * q + 1]),
+                   "r"(w[4 * q + 2]), "r"(w[4 * q + 3]) : "memory");
+}
 TW_DEV void slab_write(uint32_t slab, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -216,13 +221,11 @@ struct EpiWarp {
   int warp, lane, q, half, rank;  // index among the epilogue warps; lane quarter; column half
   int pair, pairs;
   uint32_t slabs;     // its staging
-  uint64_t* loaded;   // its two barriers of staged loads
+  uint64_t* loaded;   // its barrier of staged loads
   volatile int* abort;
   uint64_t timeout_ns;
   TW_DEV int row0(const Tile& t) const { return t.m * 2 * kBM + rank * kBM + q * 32; }
-  TW_DEV uint32_t slab(int turn, int which) const {
-    return slabs + turn * kTurnBytes + which * kSlabBytes;
-  }
+  TW_DEV uint32_t slab(int i) const { return slabs + i * kSlabBytes; }
 };
 
 // ---------------------------------------------------------------- epilogues --
@@ -232,13 +235,13 @@ struct EpiWarp {
 //   kBMN    B is MN-major: B[n][k] read from a [K][N] row-major tensor
 //   kDualK  the reduction runs over (a[0], b[0]) and then (a[1], b[1])
 //   kGroup  independent products of one shape, (a[p], b[p]) -> out[p]
-//   kStaged the epilogue goes through staging slabs
+//   kStages, kSlabs  stages of the ring, and staging slabs of an epilogue warp
 // begin() comes before the first tile, run() once a tile (false: a wait ran out),
 // end() after the last.
-template <bool DUALB, bool AMN, bool BMN, bool DUALK, bool GROUP, bool STAGED>
+template <bool DUALB, bool AMN, bool BMN, bool DUALK, bool GROUP, int STAGES, int SLABS>
 struct Operands {
-  static constexpr bool kDualB = DUALB, kAMN = AMN, kBMN = BMN, kDualK = DUALK, kGroup = GROUP,
-                        kStaged = STAGED;
+  static constexpr bool kDualB = DUALB, kAMN = AMN, kBMN = BMN, kDualK = DUALK, kGroup = GROUP;
+  static constexpr int kStages = STAGES, kSlabs = SLABS;
   static constexpr int kStep = DUALB ? 128 : kBN;  // output columns a tile
 };
 
@@ -248,11 +251,11 @@ TW_DEV void clear(const EpiWarp& w, uint32_t* words, int n) {
     for (int i = w.lane; i < n; i += 32) words[i] = 0u;
 }
 
-// h = act(z) u from the unrounded z and u; z and u are kept (bf16) for the backward
-// where it asks for them.
-struct EpiGateUp : Operands<true, false, false, false, false, true> {
+// h = act(z) u from the unrounded z and u; with KEEP z and u are kept (bf16) for the
+// backward.  Slabs: h, z, u once, or h alone in turns of two.
+template <bool KEEP>
+struct EpiGateUp : Operands<true, false, false, false, false, KEEP ? 5 : 6, KEEP ? 3 : 2> {
   int T, F, act;
-  bool keep;
   uint32_t* arrived;  // the next product's arrival counters, cleared here
   int n_arrived;
   // maps.e: h, z, u
@@ -276,20 +279,7 @@ struct EpiGateUp : Operands<true, false, false, false, false, true> {
       __syncwarp();
       tmem_ld_32x32b_x32(taddr + c, zr);
       tmem_ld_32x32b_x32(taddr + 128 + c, ur);
-      // the stores of this turn's last use have read its slabs
-      if (w.lane == 0) stores_read<1>();
-      __syncwarp();
       tmem_ld_wait();
-      if (keep) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          out[i] = pack_bf16x2(__uint_as_float(zr[2 * i]), __uint_as_float(zr[2 * i + 1]));
-        slab_write(w.slab(s.turn, 1), w.lane, out);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          out[i] = pack_bf16x2(__uint_as_float(ur[2 * i]), __uint_as_float(ur[2 * i + 1]));
-        slab_write(w.slab(s.turn, 2), w.lane, out);
-      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float a0, a1, da;
@@ -297,14 +287,28 @@ struct EpiGateUp : Operands<true, false, false, false, false, true> {
         activate<ACT>(__uint_as_float(zr[2 * i + 1]), a1, da);
         out[i] = pack_bf16x2(a0 * __uint_as_float(ur[2 * i]), a1 * __uint_as_float(ur[2 * i + 1]));
       }
-      slab_write(w.slab(s.turn, 0), w.lane, out);
+      // the last stores from these slabs have read them
+      if (w.lane == 0) stores_read<KEEP ? 0 : 1>();
+      __syncwarp();
+      const uint32_t h = w.slab(KEEP ? 0 : s.turn);
+      slab_write(h, w.lane, out);
+      if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          out[i] = pack_bf16x2(__uint_as_float(zr[2 * i]), __uint_as_float(zr[2 * i + 1]));
+        slab_write(w.slab(1), w.lane, out);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          out[i] = pack_bf16x2(__uint_as_float(ur[2 * i]), __uint_as_float(ur[2 * i + 1]));
+        slab_write(w.slab(2), w.lane, out);
+      }
       fence_async_proxy();
       __syncwarp();
       if (w.lane == 0) {  // rows and columns past the end are not stored
-        tma_store(&maps.e[0], w.slab(s.turn, 0), col, row0);
-        if (keep) {
-          tma_store(&maps.e[1], w.slab(s.turn, 1), col, row0);
-          tma_store(&maps.e[2], w.slab(s.turn, 2), col, row0);
+        tma_store(&maps.e[0], h, col, row0);
+        if (KEEP) {
+          tma_store(&maps.e[1], w.slab(1), col, row0);
+          tma_store(&maps.e[2], w.slab(2), col, row0);
         }
         stores_commit();
       }
@@ -328,44 +332,49 @@ struct EpiGateUp : Operands<true, false, false, false, false, true> {
 
 // From dh and the kept z and u: h again (bf16, the operand of dWd: keeping z and u
 // alone holds a third less between the passes), du = dh act(z), dz = dh u act'(z).
-// z and u of the next 32 columns are loaded while these are worked on; du and dz are
-// written over the z and u they came from.
-struct EpiBackward : Operands<false, false, false, false, false, true> {
+// Slabs: z, u, loaded for the next 32 columns as soon as these are in registers; h,
+// du, dz.
+struct EpiBackward : Operands<false, false, false, false, false, 4, 5> {
   int T, F, act;
   uint32_t* arrived;  // as in EpiGateUp
   int n_arrived;
   // maps.e: h, z, u, du, dz
   struct State {
-    uint32_t chunk;          // chunks worked on: turn chunk & 1, its barrier's phase (chunk >> 1) & 1
-    int next_tile, next_c;   // the chunk to load next (next_tile >= count: none)
-    uint32_t ahead;          // chunks loaded
+    uint32_t chunk;            // 32-column chunks worked on; the barrier's phase is chunk & 1
+    int next_tile;             // the chunk to load next (next_tile >= count: none):
+    int next_c;                // its column in the warp's half of the tile,
+    int next_col, next_row;    // the half's first column and the warp's first row
   };
-  // Moves the cursor to the first chunk at or behind it that has rows and columns.
+  TW_DEV void place(State& s, const EpiWarp& w, const Tiles& tiles) const {
+    const Tile t = tiles.at(s.next_tile, kStep);
+    s.next_col = t.col + w.half * 128;
+    s.next_row = w.row0(t);
+  }
+  // Moves on to the first chunk at or behind next_c that has rows and columns.
   TW_DEV void seek(State& s, const EpiWarp& w, const Tiles& tiles) const {
-    for (; s.next_tile < tiles.count; s.next_tile += w.pairs, s.next_c = 0) {
-      const Tile t = tiles.at(s.next_tile, kStep);
-      if (s.next_c < 128 && w.row0(t) < T && t.col + w.half * 128 + s.next_c < F) return;
+    while (s.next_tile < tiles.count) {
+      if (s.next_c < 128 && s.next_row < T && s.next_col + s.next_c < F) return;
+      s.next_tile += w.pairs;
+      s.next_c = 0;
+      if (s.next_tile < tiles.count) place(s, w, tiles);
     }
   }
   TW_DEV void load_next(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles) const {
     if (s.next_tile >= tiles.count) return;
     if (w.lane == 0) {
-      const Tile t = tiles.at(s.next_tile, kStep);
-      const int turn = s.ahead & 1, col = t.col + w.half * 128 + s.next_c;
-      stores_read<0>();  // the slabs' last stores have been read
-      mbar_arrive_expect_tx(&w.loaded[turn], 2 * kSlabBytes);
-      tma_load_own(w.slab(turn, 1), &maps.e[1], &w.loaded[turn], col, w.row0(t));
-      tma_load_own(w.slab(turn, 2), &maps.e[2], &w.loaded[turn], col, w.row0(t));
+      mbar_arrive_expect_tx(w.loaded, 2 * kSlabBytes);
+      tma_load_own(w.slab(0), &maps.e[1], w.loaded, s.next_col + s.next_c, s.next_row);
+      tma_load_own(w.slab(1), &maps.e[2], w.loaded, s.next_col + s.next_c, s.next_row);
     }
-    ++s.ahead;
     s.next_c += 32;
     seek(s, w, tiles);
   }
   TW_DEV void begin(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles) const {
     clear(w, arrived, n_arrived);
-    s.chunk = s.ahead = 0;
+    s.chunk = 0;
     s.next_tile = w.pair;
     s.next_c = 0;
+    if (s.next_tile < tiles.count) place(s, w, tiles);
     seek(s, w, tiles);
     load_next(s, w, maps, tiles);
   }
@@ -378,40 +387,48 @@ struct EpiBackward : Operands<false, false, false, false, false, true> {
     for (int c = w.half * 128; c < w.half * 128 + 128; c += 32) {
       const int col = t.col + c;
       if (col >= F) break;
-      const int turn = s.chunk & 1;
+      uint32_t zw[16], uw[16];
+      bool ok = mbar_wait(w.loaded, s.chunk & 1u, w.abort, w.timeout_ns);
+      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+      slab_read(w.slab(0), w.lane, zw);
+      slab_read(w.slab(1), w.lane, uw);
+      ++s.chunk;
+      __syncwarp();  // all lanes have read
       load_next(s, w, maps, tiles);
-      uint32_t r[32], zw[16], uw[16], hw[16];
-      __syncwarp();
-      tmem_ld_32x32b_x32(taddr + c, r);
-      bool ok = mbar_wait(&w.loaded[turn], (s.chunk >> 1) & 1u, w.abort, w.timeout_ns);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tmem_ld_wait();
-      if (!ok) return false;
-      slab_read(w.slab(turn, 1), w.lane, zw);
-      slab_read(w.slab(turn, 2), w.lane, uw);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float dh0 = __uint_as_float(r[2 * i]), dh1 = __uint_as_float(r[2 * i + 1]);
-        const float u0 = bf16_lo(uw[i]), u1 = bf16_hi(uw[i]);
-        float a0, a1, d0, d1;
-        activate<ACT>(bf16_lo(zw[i]), a0, d0);
-        activate<ACT>(bf16_hi(zw[i]), a1, d1);
-        hw[i] = pack_bf16x2(a0 * u0, a1 * u1);
-        uw[i] = pack_bf16x2(dh0 * a0, dh1 * a1);
-        zw[i] = pack_bf16x2(dh0 * u0 * d0, dh1 * u1 * d1);
+      for (int part = 0; part < 2; ++part) {  // 16 columns at a time, for the registers
+        uint32_t r[16], hw[8], duw[8], dzw[8];
+        __syncwarp();
+        tmem_ld_x16(taddr + c + part * 16, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float dh0 = __uint_as_float(r[2 * i]), dh1 = __uint_as_float(r[2 * i + 1]);
+          const uint32_t zp = zw[part * 8 + i], up = uw[part * 8 + i];
+          const float u0 = bf16_lo(up), u1 = bf16_hi(up);
+          float a0, a1, d0, d1;
+          activate<ACT>(bf16_lo(zp), a0, d0);
+          activate<ACT>(bf16_hi(zp), a1, d1);
+          hw[i] = pack_bf16x2(a0 * u0, a1 * u1);
+          duw[i] = pack_bf16x2(dh0 * a0, dh1 * a1);
+          dzw[i] = pack_bf16x2(dh0 * u0 * d0, dh1 * u1 * d1);
+        }
+        if (part == 0) {  // the last stores have read their slabs
+          if (w.lane == 0) stores_read<0>();
+          __syncwarp();
+        }
+        slab_write16(w.slab(2), w.lane, part * 2, hw);
+        slab_write16(w.slab(3), w.lane, part * 2, duw);
+        slab_write16(w.slab(4), w.lane, part * 2, dzw);
       }
-      slab_write(w.slab(turn, 0), w.lane, hw);
-      slab_write(w.slab(turn, 1), w.lane, zw);
-      slab_write(w.slab(turn, 2), w.lane, uw);
       fence_async_proxy();
       __syncwarp();
       if (w.lane == 0) {
-        tma_store(&maps.e[0], w.slab(turn, 0), col, row0);
-        tma_store(&maps.e[4], w.slab(turn, 1), col, row0);
-        tma_store(&maps.e[3], w.slab(turn, 2), col, row0);
+        tma_store(&maps.e[0], w.slab(2), col, row0);
+        tma_store(&maps.e[3], w.slab(3), col, row0);
+        tma_store(&maps.e[4], w.slab(4), col, row0);
         stores_commit();
       }
-      ++s.chunk;
     }
     return true;
   }
@@ -501,18 +518,26 @@ struct EpiStore : Ops {
     const float4* all = reinterpret_cast<const float4*>(parts + (size_t)place * S * kPlace) + w.lane;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
+      float4 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = __ldcg(all + (c * 8 + q) * 32);
+#pragma unroll 1
+      for (int k = 1; k < S; ++k) {
+        float4 o[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] = __ldcg(all + (size_t)k * (kPlace / 4) + (c * 8 + q) * 32);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[q].x += o[q].x; v[q].y += o[q].y; v[q].z += o[q].z; v[q].w += o[q].w;
+        }
+      }
       uint32_t r[32];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < S; ++k) {
-          const float4 o = __ldcg(all + (size_t)k * (kPlace / 4) + (c * 8 + q) * 32);
-          v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-        }
-        r[4 * q] = __float_as_uint(v.x);
-        r[4 * q + 1] = __float_as_uint(v.y);
-        r[4 * q + 2] = __float_as_uint(v.z);
-        r[4 * q + 3] = __float_as_uint(v.w);
+        r[4 * q] = __float_as_uint(v[q].x);
+        r[4 * q + 1] = __float_as_uint(v[q].y);
+        r[4 * q + 2] = __float_as_uint(v[q].z);
+        r[4 * q + 3] = __float_as_uint(v[q].w);
       }
       if (col0 + c * 32 < N) store(t, w.row0(t) + w.lane, col0 + c * 32, r);
     }
@@ -538,21 +563,21 @@ struct EpiStore : Ops {
   }
   TW_DEV void end(State&, const EpiWarp&) const {}
 };
-using OpsDown = Operands<false, false, true, false, false, false>;
-using OpsDx = Operands<false, false, true, true, false, false>;
-using OpsGrads = Operands<false, true, true, false, true, false>;
+using OpsDown = Operands<false, false, true, false, false, 6, 0>;
+using OpsDx = Operands<false, false, true, true, false, 6, 0>;
+using OpsGrads = Operands<false, true, true, false, true, 6, 0>;
 
 // ------------------------------------------------------------------- kernel --
 template <class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_gemm_kernel(const __grid_constant__ Maps maps, const Tiles tiles, const Epi epi,
                      int32_t* status, unsigned long long timeout_ns) {
-  constexpr int kStages = Layout<Epi>::kStages;
+  constexpr int kStages = Epi::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = smem + Layout<Epi>::kRing;
-  auto* sm = reinterpret_cast<Tail*>(staging + Layout<Epi>::kStaging);
+  uint8_t* slabs = smem + Layout<Epi>::kRing;
+  auto* sm = reinterpret_cast<Tail*>(slabs + Layout<Epi>::kStaging);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cta_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -568,10 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&sm->tmem_empty[a], 2 * kEpiWarps);
     }
     mbar_init(&sm->drain, 1);
-    for (int w = 0; w < kEpiWarps; ++w) {
-      mbar_init(&sm->loaded[w][0], 1);
-      mbar_init(&sm->loaded[w][1], 1);
-    }
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&sm->loaded[w], 1);
     sm->abort = 0;
     sm->never = 0;
     fence_mbar_init();
@@ -699,8 +721,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     w.rank = rank;
     w.pair = pair;
     w.pairs = pairs;
-    w.slabs = smem_u32(staging) + w.warp * 2 * kTurnBytes;
-    w.loaded = sm->loaded[w.warp];
+    w.slabs = smem_u32(slabs) + w.warp * Epi::kSlabs * kSlabBytes;
+    w.loaded = &sm->loaded[w.warp];
     w.abort = abort;
     w.timeout_ns = timeout_ns;
     typename Epi::State state;
@@ -838,17 +860,17 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
       (z && !map_slab(&m1.e[2], u, T, F)) || !map_k(&m2.a[0], h, T, F) ||
       !map_mn(&m2.b[0], Wd, F, d))
     return cudaErrorInvalidValue;
-  EpiGateUp e1;
-  e1.T = T;
-  e1.F = F;
-  e1.act = act;
-  e1.keep = z != nullptr;
+  const Tiles t1 = plan_tiles(div_up(T, 2 * kBM), div_up(F, 128), 1, div_up(d, kBK), false);
   const Tiles t2 = down_tiles(T, d, F);
-  e1.arrived = static_cast<uint32_t*>(split);
-  e1.n_arrived = counters_of(t2);
-  cudaError_t e = launch_pairs(
-      m1, plan_tiles(div_up(T, 2 * kBM), div_up(F, 128), 1, div_up(d, kBK), false), e1, status,
-      stream);
+  auto gate_up = [&](auto epi) {
+    epi.T = T;
+    epi.F = F;
+    epi.act = act;
+    epi.arrived = static_cast<uint32_t*>(split);
+    epi.n_arrived = counters_of(t2);
+    return launch_pairs(m1, t1, epi, status, stream);
+  };
+  cudaError_t e = z ? gate_up(EpiGateUp<true>{}) : gate_up(EpiGateUp<false>{});
   if (e != cudaSuccess) return e;
   EpiStore<OpsDown> e2;
   e2.M = T;
