@@ -100,7 +100,7 @@ TW_DEV void copy_row(uint32_t array, const void* base, bool bf16, size_t i,
                      ::"r"(to + h * N * 16), "l"(p + h * 4 * TEAM) : "memory");
   }
 }
-// Columns past d read what is in their place: zeros that zero_ring() left there.
+// Columns past d read what is in their place: zeros that zero_past() left there.
 template <int N>
 TW_DEV void read_row(uint32_t array, bool bf16, float (&x)[kQ][4]) {
   if (bf16) {
@@ -145,15 +145,22 @@ struct Ring {
   int y, r, dr, dn, gate, p, bytes, stages;
 };
 
-// Rows narrower than the team's columns: the places past d, which no copy writes,
-// are cleared once (with the rest; the threads meet before the first copy).
-template <int TEAM, int N>
-TW_DEV void zero_ring(uint32_t base, const Ring& ring, int d) {
-  if (d == TEAM * 4 * kQ) return;
-  const int total = ring.bytes * ring.stages;
-  for (int i = threadIdx.x * 16; i < total; i += N * 16)
-    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + i), "r"(0u) : "memory");
-  __syncthreads();
+// Rows narrower than the team's columns: a thread clears its places past d, which no
+// copy writes.
+template <int N>
+TW_DEV void zero_past(uint32_t base, const Ring& ring, int array, bool bf16,
+                      const bool (&in)[kQ]) {
+  if (array < 0 || in[kQ - 1]) return;
+  for (int s = 0; s < ring.stages; ++s) {
+#pragma unroll
+    for (int h = 0; h < kQ; ++h) {
+      const uint32_t at =
+          base + s * ring.bytes + array + (h * N + threadIdx.x) * (bf16 ? 8 : 16);
+      if (in[h]) continue;
+      if (bf16) asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(at), "r"(0u) : "memory");
+      else asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+    }
+  }
 }
 
 struct Block {
@@ -225,7 +232,9 @@ __global__ void __launch_bounds__(fwd_threads(TEAM), TEAM <= 256 ? 2 : 1)
   const long long stride = (long long)gridDim.x * TEAMS;
   const long long first = (long long)blockIdx.x * TEAMS + tm.index;
   const uint32_t base = smem_u32(rows);
-  zero_ring<TEAM, N>(base, ring, b.d);
+  zero_past<N>(base, ring, ring.y, b.y_bf16, tm.in);
+  zero_past<N>(base, ring, ring.r, b.r_bf16, tm.in);
+  zero_past<N>(base, ring, ring.gate, b.w_bf16, tm.in);
   pdl_wait();
   pdl_launch_next();
   const bool gate_rows = b.gate && b.gate_group < b.T;
@@ -325,8 +334,9 @@ __global__ void __launch_bounds__(fwd_threads(TEAM), TEAM <= 256 ? 2 : 1)
 // ----------------------------------------------------------------- backward --
 // Rows are dealt out in items: at most rows_per_item consecutive rows of one gate
 // group (per_group items cover a group).  An item belongs to a CTA, whose teams
-// share its rows, or with short groups (by_team) to one team; either way the gate
-// row's gradient is complete, or one partial of per_group, when the item is done.
+// share its rows, or to one team (by_team: with short groups, and where a CTA is one
+// team); either way the gate row's gradient is complete, or one partial of
+// per_group, when the item is done.
 struct Items {
   int group, rows_per_item, per_group, count;
   bool by_team;
@@ -341,10 +351,9 @@ struct BackwardArgs {
   float* part_pre;   // [CTAs][d]
 };
 
-// Shared memory behind the ring (byte offsets): w_pre in fp32; with gate rows, each
-// thread's sums of dw_post over the items done, and (teams but the first) what the
-// first team adds up.  Without gate rows that is only done behind the loop, in the
-// ring's place.
+// Shared memory behind the ring (byte offsets): w_pre in fp32; with gate rows, the sums
+// of dw_post over the items done (of a thread, or of the CTA's columns) and the teams'
+// sums of an item.  Sums over the teams behind the loop take the ring's place.
 struct Extra {
   int wpre, post, comb;
 };
@@ -371,7 +380,11 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
   const uint32_t base = smem_u32(rows);
   const bool gate_rows = b.gate && it.group < b.T;
   const bool gate_ring = gate_rows && ring.gate >= 0;
-  zero_ring<TEAM, N>(base, ring, b.d);
+  zero_past<N>(base, ring, ring.y, b.y_bf16, tm.in);
+  zero_past<N>(base, ring, ring.r, b.r_bf16, tm.in);
+  zero_past<N>(base, ring, ring.gate, b.w_bf16, tm.in);
+  zero_past<N>(base, ring, ring.dr, b.r_bf16, tm.in);
+  zero_past<N>(base, ring, ring.dn, b.n_bf16, tm.in);
   pdl_wait();
   pdl_launch_next();
 
@@ -436,23 +449,36 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
   auto mine = [&](int array, int h) {
     return reinterpret_cast<float4*>(rows + array) + h * N + threadIdx.x;
   };
-  // Adds a vector over the teams into the first team's registers (all threads).
-  auto combine = [&](float (&v)[kQ][4]) {
-    if (TEAMS == 1) return;
-    float4* comb = reinterpret_cast<float4*>(rows + (gate_rows ? extra.comb : 0));
-    __syncthreads();
-    if (tm.index > 0) {
+  // Sums over the teams: every thread leaves its columns in an area, and after a barrier
+  // a thread takes strips of 4 columns, strip i being columns 4i..4i+3.
+  constexpr int kStrips = kQ * TEAM;
+  auto leave = [&](int array, const float (&v)[kQ][4]) {
 #pragma unroll
-      for (int h = 0; h < kQ; ++h) comb[h * N + threadIdx.x - TEAM] = vec4(v[h]);
+    for (int h = 0; h < kQ; ++h) *mine(array, h) = vec4(v[h]);
+  };
+  auto strip_sum = [&](int array, int i, float (&v)[4]) {
+    const float4* at = reinterpret_cast<const float4*>(rows + array) + (i / TEAM) * N + i % TEAM;
+    v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll 4
+    for (int t = 0; t < TEAMS; ++t) {
+      const float4 o = at[t * TEAM];
+      v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
     }
-    __syncthreads();
-    if (tm.index == 0)
-      for (int t = 0; t + 1 < TEAMS; ++t)
-#pragma unroll
-        for (int h = 0; h < kQ; ++h) {
-          const float4 o = comb[h * N + t * TEAM + tm.tid];
-          v[h][0] += o.x; v[h][1] += o.y; v[h][2] += o.z; v[h][3] += o.w;
-        }
+  };
+  auto strip_load = [&](const void* w, size_t at, float (&v)[4]) {
+    v[0] = v[1] = v[2] = v[3] = 1.f;
+    if (!w) return;
+    if (b.w_bf16) {
+      unpack4(*reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at), v);
+    } else {
+      const float4 o = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
+      v[0] = o.x; v[1] = o.y; v[2] = o.z; v[3] = o.w;
+    }
+  };
+  // s x times y of a strip to global memory.
+  auto strip_store = [&](float* to, int i, const float (&x)[4], const float (&y)[4]) {
+    *reinterpret_cast<float4*>(to + 4 * i) = make_float4(
+        b.s * x[0] * y[0], b.s * x[1] * y[1], b.s * x[2] * y[2], b.s * x[3] * y[3]);
   };
 
   const bool keep_post = g.part_post && gate_rows;
@@ -565,13 +591,13 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
       }
     }
     if (gate_rows) {
-      if (!it.by_team) combine(A);
-      if (it.by_team || tm.index == 0) {
+      float* to = g.dgate + (size_t)(it.per_group == 1 ? group : item) * b.d;
+      if (it.by_team) {
         float w[kQ][4], gt[kQ][4];
         ones(w);
         ones(gt);
         if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
-        if (b.gate) load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, gt);
+        load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, gt);
 #pragma unroll
         for (int h = 0; h < kQ; ++h) {
           if (keep_post) {
@@ -585,8 +611,23 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[h][k] *= b.s * A[h][k];
         }
-        store_row<TEAM>(g.dgate + (size_t)(it.per_group == 1 ? group : item) * b.d, false,
-                        4 * tm.tid, tm.in, w);
+        store_row<TEAM>(to, false, 4 * tm.tid, tm.in, w);
+      } else {
+        __syncthreads();  // the last item's sums have been taken
+        leave(extra.comb, A);
+        __syncthreads();
+        for (int i = threadIdx.x; i < kStrips && 4 * i < b.d; i += N) {
+          float w[4], gt[4], v[4];
+          strip_load(b.w_post, 4 * i, w);
+          strip_load(b.gate, (size_t)group * b.d + 4 * i, gt);
+          strip_sum(extra.comb, i, v);
+          strip_store(to, i, w, v);
+          if (keep_post) {  // the strip is this thread's in every item
+            float4* o = reinterpret_cast<float4*>(rows + extra.post) + i;
+            *o = make_float4(fmaf(b.s * gt[0], v[0], o->x), fmaf(b.s * gt[1], v[1], o->y),
+                             fmaf(b.s * gt[2], v[2], o->z), fmaf(b.s * gt[3], v[3], o->w));
+          }
+        }
       }
 #pragma unroll
       for (int h = 0; h < kQ; ++h)
@@ -594,44 +635,35 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
         for (int k = 0; k < 4; ++k) A[h][k] = 0.f;
     }
   }
-  // without gate rows A runs over all the CTA's rows, and gives both gradients here
-  const size_t part_at = (size_t)blockIdx.x * b.d + 4 * tm.tid;
-  if (g.part_pre) {
-    combine(apre);
-    if (tm.index == 0) store_row<TEAM>(g.part_pre, false, part_at, tm.in, apre);
-  }
-  if (keep_post) {
-#pragma unroll
-    for (int h = 0; h < kQ; ++h) {
-      const float4 o = *mine(extra.post, h);
-      A[h][0] = o.x; A[h][1] = o.y; A[h][2] = o.z; A[h][3] = o.w;
+  // Without gate rows A runs over all the CTA's rows, and gives both gradients here.
+  constexpr int kVector = 4 * 4 * kQ * N;  // bytes of an area
+  __syncthreads();  // the ring's rows have been read
+  if (g.part_pre) leave(0, apre);
+  if (!gate_rows) leave(kVector, A);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kStrips && 4 * i < b.d; i += N) {
+    const size_t part_at = (size_t)blockIdx.x * b.d;
+    float w[4], gt[4], v[4];
+    if (!gate_rows) {
+      strip_load(b.w_post, 4 * i, w);
+      strip_load(b.gate, 4 * i, gt);
     }
-    combine(A);
-    if (tm.index == 0) store_row<TEAM>(g.part_post, false, part_at, tm.in, A);
-  } else if (!gate_rows && (b.gate || g.part_post)) {
-    combine(A);
-    if (tm.index == 0) {
-      float w[kQ][4];
-      ones(w);
-      if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
-      if (b.gate) {
-#pragma unroll
-        for (int h = 0; h < kQ; ++h)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) F[h][k] = b.s * A[h][k] * w[h][k];
-        store_row<TEAM>(g.dgate, false, part_at, tm.in, F);
-        ones(w);
-        load_row<TEAM>(b.gate, b.w_bf16, 4 * tm.tid, tm.in, w);
+    if (g.part_pre) {
+      strip_sum(0, i, v);
+      *reinterpret_cast<float4*>(g.part_pre + part_at + 4 * i) = vec4(v);
+    }
+    if (keep_post) {
+      if (it.by_team) {
+        strip_sum(extra.post, i, v);
       } else {
-        ones(w);
+        const float4 o = reinterpret_cast<const float4*>(rows + extra.post)[i];
+        v[0] = o.x; v[1] = o.y; v[2] = o.z; v[3] = o.w;
       }
-      if (g.part_post) {
-#pragma unroll
-        for (int h = 0; h < kQ; ++h)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) A[h][k] *= b.s * w[h][k];
-        store_row<TEAM>(g.part_post, false, part_at, tm.in, A);
-      }
+      *reinterpret_cast<float4*>(g.part_post + part_at + 4 * i) = vec4(v);
+    } else if (!gate_rows) {
+      strip_sum(kVector, i, v);
+      if (b.gate) strip_store(g.dgate + part_at, i, w, v);
+      if (g.part_post) strip_store(g.part_post + part_at, i, gt, v);
     }
   }
 }
@@ -711,8 +743,9 @@ Plan make_plan(int T, int d, int gate_group, int sms) {
   const int group = gate_group <= 0 || gate_group > T ? (T > 0 ? T : 1) : gate_group;
   const int groups = (int)((T64 + group - 1) / group);
   p.it.group = group;
-  p.it.by_team = group < kShortGroup && groups > 1;
-  if (p.it.by_team) {
+  const bool short_groups = group < kShortGroup && groups > 1;
+  p.it.by_team = short_groups || teams == 1;
+  if (short_groups) {
     p.it.per_group = 1;
     p.it.rows_per_item = group;
   } else {
@@ -796,7 +829,9 @@ cudaError_t forward_team(const Block& k, const void* y, const void* r, void* r_o
                          float* rstd_post, float* rstd_pre, cudaStream_t stream) {
   constexpr int N = fwd_threads(TEAM), TEAMS = N / TEAM, per_sm = TEAM <= 256 ? 2 : 1;
   const long long want = ((long long)k.T + TEAMS - 1) / TEAMS;
-  const long long most = (long long)num_sms() * per_sm;
+  // CTAs for four rounds: one round of CTAs with more rows each takes 74 us for 16384 x
+  // 2048 against 65, and eight take 75
+  const long long most = (long long)num_sms() * per_sm * 4;
   const bool gate_rows = k.gate && k.gate_group < k.T;
   const int w = k.w_bf16 ? 2 : 4;
   const Ring ring = make_ring(N, !y ? 0 : k.y_bf16 ? 2 : 4, k.r_bf16 ? 2 : 4, 0, 0,
@@ -819,7 +854,7 @@ cudaError_t backward_team(const Block& k, const BackwardArgs& g, const Plan& p,
   const int vector = 4 * 4 * kQ * N;  // fp32 columns of every thread
   const int wpre = k.w_pre ? 4 * 4 * kQ * TEAM : 0;
   const int post = gate_rows && g.part_post ? vector : 0;
-  const int comb = gate_rows && TEAMS > 1 ? vector : 0;
+  const int comb = gate_rows && !p.it.by_team ? vector : 0;
   // the widest rows' gate rows are read when they are needed, not ahead: with fp32
   // arrays they would not fit
   const Ring ring = make_ring(N, !g.y ? 0 : k.y_bf16 ? 2 : 4, g.dn ? r : 0,
@@ -828,7 +863,7 @@ cudaError_t backward_team(const Block& k, const BackwardArgs& g, const Plan& p,
                               kSmemSm - wpre - post - comb);
   // the last sums over the teams take the ring's place
   int at = ring.bytes * ring.stages;
-  if (TEAMS > 1 && at < vector) at = vector;
+  if (at < 2 * vector) at = 2 * vector;
   Extra x;
   x.wpre = at;
   x.post = x.wpre + wpre;

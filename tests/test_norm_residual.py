@@ -343,6 +343,27 @@ def test_backward(T, d, gate):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,d,group", [(50, 8192, 7), (90, 8192, 40), (300, 8192, 300), (90, 4096, 40),
+                                       (90, 4096, 3), (200, 2048, 33), (90, 512, 40)])
+def test_all_fp32_with_gate_rows(T, d, group):
+    """The most shared memory that a width asks for."""
+    rng = np.random.default_rng(T + d + group)
+    t, got, run = _backward(rng, T, d, group, F32, F32, F32, F32, True, True, True)
+    run()
+    torch.cuda.synchronize()
+    _check_backward(t, got, group, 0.75, 0.5)
+    for k in ("r", "r_out"):
+        t[k] = t["r_out"].clone()
+    n = torch.empty_like(t["r"])
+    twell.norm_residual_forward(t["y"], t["r"], t["w_post"], t["gate"], t["w_pre"], t["r_out"], n,
+                                gate_group=group, res_scale=0.75, block_scale=0.5, eps=1e-5,
+                                rstd_post=t["p"], rstd_pre=t["q"])
+    torch.cuda.synchronize()
+    f = {k: t[k] for k in ("y", "r", "w_post", "gate", "w_pre")}
+    _check_forward(f, t["r_out"], n, t["p"], t["q"], group, 0.75, 0.5, float(np.float32(1e-5)))
+
+
+@pytest.mark.gpu
 def test_remaining_dtype_combinations():
     rng = np.random.default_rng(8)
     for yt in (BF, F32):
