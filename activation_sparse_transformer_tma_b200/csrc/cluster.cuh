@@ -35,8 +35,9 @@ TW_DEV uint32_t place_in(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-TW_DEV void store_in(uint32_t cluster_addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+TW_DEV void store_in(uint32_t cluster_addr, uint32_t v0, uint32_t v1) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(v0), "r"(v1)
+               : "memory");
 }
 
 // 32 lanes x 16 consecutive columns of tensor memory.  Warp-collective.

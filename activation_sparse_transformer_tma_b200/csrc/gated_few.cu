@@ -18,8 +18,9 @@
 // first kernel has waited for whatever came before it, and does not write Wd -- and
 // waits for the first kernel before it reads h.
 //
-// Roles (192 threads): warp 0 loads by TMA, warp 1 allocates TMEM and issues the
-// MMAs, warps 2..5 read TMEM (warp w owns lanes 32 (w % 4)..).  Every mbarrier wait is
+// Roles (320 threads): warp 0 loads by TMA, warp 1 allocates TMEM and issues the
+// MMAs, warps 2..9 read TMEM (warp w owns lanes 32 (w % 4)..) and finish the tokens; with
+// four of them the finish of 37 tokens took 5 us of the call's 33.  Every mbarrier wait is
 // bounded; the cluster barriers are reached by every thread after bounded work.
 #include "tmap.h"
 #include "pdl.cuh"
@@ -36,7 +37,8 @@ constexpr int kRows = 128;                 // rows of weights a tile (MMA M)
 constexpr int kUnits = 64;                 // units a gate-up tile
 constexpr int kWBytes = kRows * kBK * 2;   // weights a stage
 constexpr int kMaxStages = 6;
-constexpr int kThreads = 192;
+constexpr int kEndWarps = 8;                // two a quarter of the TMEM lanes
+constexpr int kThreads = 64 + 32 * kEndWarps;
 constexpr int kMaxCluster = 8;             // portable cluster size
 
 struct Tail {
@@ -198,24 +200,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   // all the cluster's products are done: the rings are free for the exchange
   cluster_meet();
-  const int part = f.N / ranks;  // tokens a CTA finishes
+  const int part = f.N / ranks, pairs = part / 2;  // tokens a CTA finishes, and pairs of them
   const uint32_t exchange = smem_u32(smem);
   if (warp >= 2 && !*abort) {
     const int row = (warp & 3) * 32 + lane;
     const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    // column by column to the CTA that finishes the token
-    const uint32_t mine = exchange + ((rank * part * kRows + row) << 2);
-    int to = 0, at = 0;
-    uint32_t place = place_in(mine, 0);
-    for (int c = 0; c < f.N; c += 16) {
+    // two tokens at a time to the CTA that finishes them (part is even); a source's
+    // sums of token pair p and row r are at [source][p][r]
+    const uint32_t mine = exchange + ((rank * pairs * kRows + row) << 3);
+    for (int c = ((warp - 2) >> 2) * 16; c < f.N; c += 32) {
+      int to = c / part, p = (c - to * part) / 2;
+      uint32_t place = place_in(mine, to);
       uint32_t r[16];
       tmem_ld_x16(taddr + c, r);
       tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        store_in(place + at * (kRows * 4), __uint_as_float(r[k]));
-        if (++at == part) {
-          at = 0;
+      for (int k = 0; k < 16; k += 2) {
+        store_in(place + p * (kRows * 8), r[k], r[k + 1]);
+        if (++p == pairs) {
+          p = 0;
           if (++to < ranks) place = place_in(mine, to);
         }
       }
@@ -226,35 +229,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_meet();
   if (warp >= 2 && !*abort) {
     const int th = threadIdx.x - 64;
-    const float* sums = reinterpret_cast<const float*>(smem);
-    auto total = [&](int at, int row) {
-      float v = 0.f;
-      for (int s = 0; s < ranks; ++s) v += sums[(s * part + at) * kRows + row];
+    const float2* sums = reinterpret_cast<const float2*>(smem);
+    auto total = [&](int p, int row) {
+      float2 v = make_float2(0.f, 0.f);
+      for (int s = 0; s < ranks; ++s) {
+        const float2 o = sums[(s * pairs + p) * kRows + row];
+        v.x += o.x;
+        v.y += o.y;
+      }
       return v;
     };
     if (DOWN) {
-      const int col = tile * kRows + th;
+      const int row = th & (kRows - 1), col = tile * kRows + row;
       if (col < f.width)
-        for (int at = 0; at < part; ++at) {
-          const int t = rank * part + at;
-          if (t >= f.T) break;
-          const float v = total(at, th);
-          const size_t to = (size_t)t * f.width + col;
-          if (f.y_bf16) static_cast<uint16_t*>(f.y)[to] = f32_to_bf16(v);
-          else static_cast<float*>(f.y)[to] = v;
+        for (int p = th / kRows; p < pairs; p += 32 * kEndWarps / kRows) {
+          const float2 v = total(p, row);
+          const float v2[2] = {v.x, v.y};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = rank * part + 2 * p + k;
+            if (t >= f.T) continue;
+            const size_t to = (size_t)t * f.width + col;
+            if (f.y_bf16) static_cast<uint16_t*>(f.y)[to] = f32_to_bf16(v2[k]);
+            else static_cast<float*>(f.y)[to] = v2[k];
+          }
         }
     } else {
-      const int unit = tile * kUnits + (th & 63);
+      const int row = th & (kUnits - 1), unit = tile * kUnits + row;
       if (unit < f.width)
-        for (int at = th >> 6; at < part; at += 2) {
-          const int t = rank * part + at;
-          if (t >= f.T) break;
-          const float z = total(at, th & 63), u = total(at, kUnits + (th & 63));
-          const size_t to = (size_t)t * f.width + unit;
-          f.h[to] = f32_to_bf16(activated(f.act, z) * u);
-          if (f.z) {
-            f.z[to] = f32_to_bf16(z);
-            f.u[to] = f32_to_bf16(u);
+        for (int p = th / kUnits; p < pairs; p += 32 * kEndWarps / kUnits) {
+          const float2 z = total(p, row), u = total(p, kUnits + row);
+          const float z2[2] = {z.x, z.y}, u2[2] = {u.x, u.y};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = rank * part + 2 * p + k;
+            if (t >= f.T) continue;
+            const size_t to = (size_t)t * f.width + unit;
+            f.h[to] = f32_to_bf16(activated(f.act, z2[k]) * u2[k]);
+            if (f.z) {
+              f.z[to] = f32_to_bf16(z2[k]);
+              f.u[to] = f32_to_bf16(u2[k]);
+            }
           }
         }
     }

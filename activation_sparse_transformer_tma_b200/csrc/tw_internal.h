@@ -141,7 +141,7 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
 size_t gated_forward_split_bytes(int T, int d, int F);
 size_t gated_backward_split_bytes(int T, int d, int F);
 // The same forward for few tokens (gated_few.cu).
-constexpr int kGatedFewMaxT = 128;
+constexpr int kGatedFewMaxT = 112;
 cudaError_t launch_gated_few(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
                              int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z, uint16_t* u,
                              void* y, tw_dtype y_dtype, int32_t* status, cudaStream_t stream);
