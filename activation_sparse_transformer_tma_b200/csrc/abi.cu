@@ -116,6 +116,36 @@ tw_status check_hybrid(const tw_hybrid* h) {
   return TW_OK;
 }
 
+// One array of a call.  `over`: inputs whose whole array an output may take.
+struct Span {
+  const void* at;
+  size_t bytes;
+  bool written;
+  const void* over[2];
+};
+
+// Whether no written array overlaps another one, but for the allowed whole arrays.
+template <size_t N>
+bool spans_apart(const Span (&spans)[N]) {
+  for (size_t i = 0; i < N; ++i) {
+    const Span& w = spans[i];
+    if (!w.written || !w.at || w.bytes == 0) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(w.at);
+    for (size_t j = 0; j < N; ++j) {
+      const Span& o = spans[j];
+      if (j == i || !o.at || o.bytes == 0) continue;
+      const uintptr_t b = reinterpret_cast<uintptr_t>(o.at);
+      if (a >= b + o.bytes || b >= a + w.bytes) continue;
+      if (!o.written && a == b && w.bytes == o.bytes && (o.at == w.over[0] || o.at == w.over[1]))
+        continue;
+      return false;
+    }
+  }
+  return true;
+}
+
+size_t bytes_of(tw_dtype t) { return t == TW_BF16 ? 2 : 4; }
+
 }  // namespace
 
 extern "C" {
@@ -153,7 +183,7 @@ const char* tw_status_string(tw_status s) {
   return "TW_UNKNOWN_STATUS";
 }
 
-int32_t twell_version(void) { return 100; }
+int32_t twell_version(void) { return 200; }
 
 void tw_test_withhold_next_gate_loads(uint64_t wait_limit_ns) {
   tw::g_withheld_gate_wait.store(wait_limit_ns > 0 ? wait_limit_ns : 1);
@@ -347,7 +377,14 @@ tw_status gated_ffn_forward(const void* x, const void* Wg_t, const void* Wu_t, c
   for (const void* p : ptrs)
     if (!aligned16(p)) return TW_ERR_ALIGNMENT;
   if (T == 0) return TW_OK;
-  if (ws_bytes < gated_ffn_workspace_size(T, d, F)) return TW_ERR_WORKSPACE;
+  const size_t need = gated_ffn_workspace_size(T, d, F);
+  if (ws_bytes < need) return TW_ERR_WORKSPACE;
+  const size_t rows = (size_t)T * d, acts = (size_t)T * F * 2, w = (size_t)F * d * 2;
+  const Span spans[] = {{x, rows * 2, false, {}},    {Wg_t, w, false, {}},
+                        {Wu_t, w, false, {}},        {Wd, w, false, {}},
+                        {z_save, acts, true, {}},    {u_save, acts, true, {}},
+                        {y, rows * bytes_of(y_dtype), true, {}}, {ws, need, true, {}}};
+  if (!spans_apart(spans)) return TW_ERR_INVALID_ARG;
   return from_cuda(tw::launch_gated_forward(x, Wg_t, Wu_t, Wd, T, d, F, act,
                                             static_cast<uint16_t*>(ws),
                                             static_cast<uint16_t*>(z_save),
@@ -369,8 +406,19 @@ tw_status gated_ffn_backward(const void* x, const void* dy, const void* Wg_t, co
   const void* ptrs[] = {x, dy, Wg_t, Wu_t, Wd, z_save, u_save, dx, dWg_t, dWu_t, dWd, ws};
   for (const void* p : ptrs)
     if (!aligned16(p)) return TW_ERR_ALIGNMENT;
+  const size_t need = gated_ffn_backward_workspace_size(T, d, F);
+  if (T > 0 && ws_bytes < need) return TW_ERR_WORKSPACE;
+  const size_t rows = (size_t)T * d, acts = (size_t)T * F * 2, w = (size_t)F * d;
+  const size_t dw = w * bytes_of(dw_dtype);
+  const Span spans[] = {{x, rows * 2, false, {}},  {dy, rows * 2, false, {}},
+                        {Wg_t, w * 2, false, {}},  {Wu_t, w * 2, false, {}},
+                        {Wd, w * 2, false, {}},    {z_save, acts, false, {}},
+                        {u_save, acts, false, {}}, {dx, rows * bytes_of(dx_dtype), true, {}},
+                        {dWg_t, dw, true, {}},     {dWu_t, dw, true, {}},
+                        {dWd, dw, true, {}},       {T > 0 ? ws : nullptr, need, true, {}}};
+  if (!spans_apart(spans)) return TW_ERR_INVALID_ARG;
   if (T == 0) {  // no tokens: zero weight gradients
-    const size_t bytes = (dw_dtype == TW_BF16 ? 2 : 4) * (size_t)F * d;
+    const size_t bytes = dw;
     void* grads[] = {dWg_t, dWu_t, dWd};
     for (void* g : grads) {
       cudaError_t e = cudaMemsetAsync(g, 0, bytes, stream);
@@ -378,7 +426,6 @@ tw_status gated_ffn_backward(const void* x, const void* dy, const void* Wg_t, co
     }
     return TW_OK;
   }
-  if (ws_bytes < gated_ffn_backward_workspace_size(T, d, F)) return TW_ERR_WORKSPACE;
   uint16_t* base = static_cast<uint16_t*>(ws);
   const size_t part = gated_part(T, F) / 2;
   return from_cuda(tw::launch_gated_backward(
@@ -418,6 +465,20 @@ tw_status norm_residual_forward(const tw_norm_block* b, const void* y, const voi
   if ((b->w_pre != nullptr) != (n_out != nullptr) || (rstd_pre && !b->w_pre) ||
       (rstd_post && !b->w_post))
     return TW_ERR_INVALID_ARG;
+  const size_t e = (size_t)b->T * b->d, d = (size_t)b->d * bytes_of(b->w_dtype), f = (size_t)b->T * 4;
+  const size_t groups = b->gate ? ((size_t)b->T + b->gate_group - 1) / b->gate_group : 0;
+  const bool yn = b->n_dtype == b->y_dtype, rn = b->n_dtype == b->r_dtype;
+  const Span spans[] = {{y, e * bytes_of(b->y_dtype), false, {}},
+                        {r, e * bytes_of(b->r_dtype), false, {}},
+                        {b->w_post, d, false, {}},
+                        {b->gate, groups * d, false, {}},
+                        {b->w_pre, d, false, {}},
+                        {r_out, e * bytes_of(b->r_dtype), true,
+                         {r, b->y_dtype == b->r_dtype ? y : nullptr}},
+                        {n_out, e * bytes_of(b->n_dtype), true, {yn ? y : nullptr, rn ? r : nullptr}},
+                        {rstd_post, f, true, {}},
+                        {rstd_pre, f, true, {}}};
+  if (!spans_apart(spans)) return TW_ERR_INVALID_ARG;
   return from_cuda(
       tw::launch_norm_forward(*b, y, r, r_out, n_out, rstd_post, rstd_pre, stream));
 }
@@ -454,8 +515,27 @@ tw_status norm_residual_backward(const tw_norm_block* b, const void* dn, const v
       (b->w_post != nullptr) != (rstd_post != nullptr) || (b->w_pre && !r_out))
     return TW_ERR_INVALID_ARG;
   if (!ws) return TW_ERR_INVALID_ARG;
-  if (ws_bytes < tw::norm_backward_ws_bytes(b->T, b->d, b->gate ? b->gate_group : 0))
-    return TW_ERR_WORKSPACE;
+  const size_t need = tw::norm_backward_ws_bytes(b->T, b->d, b->gate ? b->gate_group : 0);
+  if (ws_bytes < need) return TW_ERR_WORKSPACE;
+  const size_t e = (size_t)b->T * b->d, d = (size_t)b->d * bytes_of(b->w_dtype), f = (size_t)b->T * 4;
+  const size_t groups = b->gate ? ((size_t)b->T + b->gate_group - 1) / b->gate_group : 0;
+  const size_t er = e * bytes_of(b->r_dtype), ey = e * bytes_of(b->y_dtype), d4 = (size_t)b->d * 4;
+  const Span spans[] = {{dn, e * bytes_of(b->n_dtype), false, {}},
+                        {dr_out, er, false, {}},
+                        {y, ey, false, {}},
+                        {b->w_pre ? r_out : nullptr, er, false, {}},
+                        {b->w_post, d, false, {}},
+                        {b->gate, groups * d, false, {}},
+                        {b->w_pre, d, false, {}},
+                        {rstd_post, f, false, {}},
+                        {rstd_pre, f, false, {}},
+                        {dy, ey, true, {y, b->n_dtype == b->y_dtype ? dn : nullptr}},
+                        {dr, er, true, {dr_out, nullptr}},
+                        {dw_post, d4, true, {}},
+                        {dgate, groups * d4, true, {}},
+                        {dw_pre, d4, true, {}},
+                        {ws, need, true, {}}};
+  if (!spans_apart(spans)) return TW_ERR_INVALID_ARG;
   return from_cuda(tw::launch_norm_backward(*b, dn, dr_out, y, r_out, rstd_post, rstd_pre, dy, dr,
                                             dw_post, dgate, dw_pre, ws, stream));
 }

@@ -331,6 +331,7 @@ TW_API tw_status dense_ffn_train_backward(const void* x, const void* dy, const v
  * backward; both NULL for inference.
  * Limits: d % 8 == 0, F % 8 == 0, d >= 64, F >= 64, T >= 0 (with T == 0 the arrays
  * sized by T may be NULL).
+ * No written array (ws among them) may overlap another array of the call.
  * ws: at least gated_ffn_workspace_size(T, d, F) bytes, asked with the device
  * current that runs the call; calls sharing one workspace must not overlap on the device.
  */
@@ -347,6 +348,7 @@ TW_API tw_status gated_ffn_forward(const void* x, const void* Wg_t, const void* 
  *   dWd = h^T dy, dWu_t = du^T x, dWg_t = dz^T x ([F][d], dw_dtype, overwritten).
  * dy [T][d] bf16.  h (from the saved z and u), du and dz are rounded to bf16 as the
  * operands of the products; sums are fp32, in a fixed order.  act'(0) = 0 for ReLU.
+ * No written array (ws among them) may overlap another array of the call.
  * ws: at least gated_ffn_backward_workspace_size(T, d, F) bytes (h, du, dz).  With
  * T == 0 the weight gradients are zeroed.
  */
@@ -389,8 +391,8 @@ typedef struct {
 /*
  * y [T][d] (y_dtype), r and r_out [T][d] (r_dtype), n_out [T][d] (n_dtype).
  * rstd_post, rstd_pre [T] fp32: kept for the backward, NULL for inference.
- * An output may share its whole array with an input of the same dtype (r_out
- * with r, n_out with y); other overlaps are not allowed.
+ * r_out and n_out may each take the whole array of r or y, where the dtypes are equal;
+ * other overlaps are refused.
  */
 TW_API tw_status norm_residual_forward(const tw_norm_block* b, const void* y, const void* r,
                                        void* r_out, void* n_out, float* rstd_post,
@@ -408,7 +410,7 @@ TW_API tw_status norm_residual_forward(const tw_norm_block* b, const void* y, co
  * dr (r_dtype), dy (y_dtype); dw_post, dw_pre [d] and dgate [rows][d] fp32,
  * fully overwritten, summed in a fixed order (deterministic).  Without y, dy,
  * dgate and dw_post are NULL and dr = G.  dr may be dr_out, dy may be y or dn
- * (same dtype); other overlaps are not allowed.
+ * (same dtype); other overlaps are refused.
  * ws: at least norm_residual_backward_workspace_size(T, d, gate_group) bytes
  * (gate_group 0 without a gate), asked with the device current that runs the call; calls sharing
  * one workspace must not overlap on the device.

@@ -97,6 +97,33 @@ def test_refusals(L):
     assert b(n=bws - 1) == WORKSPACE
 
 
+def test_overlapping_arrays_are_refused(L):
+    names = ("x", "dy", "g", "w", "dn", "z", "u", "dx", "dg", "dw", "dd", "ws")
+    ws = L.gated_ffn_backward_workspace_size(100, 128, 256)
+
+    def at(**over):
+        a = {k: FAKE + 0x100000 * i for i, k in enumerate(names)}
+        a.update({k: a[v] + off for k, (v, off) in over.items()})
+        return a
+
+    def b(**over):
+        a = at(**over)
+        return L.gated_ffn_backward(a["x"], a["dy"], a["g"], a["w"], a["dn"], 100, 128, 256, 1,
+                                    a["z"], a["u"], a["dx"], 1, a["dg"], a["dw"], a["dd"], 0,
+                                    a["ws"], ws, None, None)
+
+    def f(**over):
+        a = at(**over)
+        return L.gated_ffn_forward(a["x"], a["g"], a["w"], a["dn"], 100, 128, 256, 1, a["z"], a["u"],
+                                   a["dx"], 1, a["ws"], ws, None, None)
+
+    for over in (dict(dx=("dy", 0)), dict(dg=("dw", 0)), dict(dd=("dn", 0)), dict(dx=("ws", 1024)),
+                 dict(ws=("z", 16)), dict(dw=("dg", 256 * 128 * 4 - 16))):
+        assert b(**over) == INVALID, over
+    for over in (dict(dx=("x", 0)), dict(z=("u", 0)), dict(ws=("dn", 0)), dict(u=("x", -16))):
+        assert f(**over) == INVALID, over
+
+
 def test_binding_refuses_wrong_tensors():
     x = torch.zeros(4, 64, dtype=BF)
     w = torch.zeros(72, 64, dtype=BF)

@@ -143,6 +143,31 @@ def test_backward_refusals(L):
     assert f(_block(), dy=FAKE + 8) == ALIGN
 
 
+def test_overlapping_arrays_are_refused(L):
+    # 10 x 64: 1280 bytes of bf16 (y, n), 2560 of fp32 (r)
+    y, r, ro, n, w = (FAKE + 0x10000 * k for k in range(5))
+    b = _block(w_post=w, w_pre=w + 0x1000)
+
+    def f(y=y, r=r, ro=ro, n=n):
+        return L.norm_residual_forward(ctypes.byref(b), y, r, ro, n, None, None, None)
+
+    assert f(ro=r + 1280) == INVALID and f(n=r) == INVALID and f(ro=y) == INVALID
+    assert f(n=w) == INVALID and f(ro=n) == INVALID and f(n=y + 16) == INVALID
+    size = L.norm_residual_backward_workspace_size(10, 64, 0)
+    names = ["dn", "dr_out", "y", "r_out", "rstd_post", "rstd_pre", "dy", "dr", "dw_post", "dgate",
+             "dw_pre", "ws"]
+
+    def g(**over):
+        a = {k: FAKE + 0x10000 * i for i, k in enumerate(names)}
+        a["dgate"] = None
+        a.update({k: a[v] for k, v in over.items()})
+        return L.norm_residual_backward(ctypes.byref(b), *[a[k] for k in names], size, None)
+
+    for k, v in (("dr", "r_out"), ("dw_post", "dw_pre"), ("ws", "y"), ("dy", "dr"), ("dr", "dn"),
+                 ("dw_pre", "rstd_pre")):
+        assert g(**{k: v}) == INVALID, (k, v)
+
+
 def test_binding_refuses_host_tensors_and_mixed_weights():
     x = torch.zeros(4, 8)
     with pytest.raises(ValueError):
