@@ -363,8 +363,13 @@ struct Extra {
 //
 // One reduction a row: with H = dr_out + rstd_pre e, the second mean is
 //   sum f yh = sum F H yh - rstd_pre mean(e rh) sum F rh yh,   F = s gate w_post,
-// so its sums need no result of the first; a second reduction behind the first
-// took 3% longer.  The terms are those that G itself is summed from.
+// so its sums need no result of the first (a second reduction behind the first cost
+// about 1 us of 67 for 8192 x 2048).  The terms are those that G is summed from.
+//
+// One CTA of 384 threads an SM: 60 us for 8192 x 2048 (302 MB, 5.0 TB/s) against 66
+// with 256 threads; 512 spill registers and leave room for one row a team (92 us).
+// Two CTAs' worth of rounds cost more (69 us): what a CTA does once, its first rows'
+// latency and its partial row, is 8 us.
 template <int TEAM>
 __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
     norm_backward_kernel(const Block b, const BackwardArgs g, const Items it, const Ring ring,
@@ -848,7 +853,7 @@ cudaError_t forward_team(const Block& k, const void* y, const void* r, void* r_o
 template <int TEAM>
 cudaError_t backward_team(const Block& k, const BackwardArgs& g, const Plan& p,
                           cudaStream_t stream) {
-  constexpr int N = bwd_threads(TEAM), TEAMS = N / TEAM;
+  constexpr int N = bwd_threads(TEAM);
   const int r = k.r_bf16 ? 2 : 4, w = k.w_bf16 ? 2 : 4;
   const bool gate_rows = k.gate && p.it.group < k.T;
   const int vector = 4 * 4 * kQ * N;  // fp32 columns of every thread
