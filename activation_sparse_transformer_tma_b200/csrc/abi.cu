@@ -2,6 +2,7 @@
 // (before any launch) and dispatch to the kernels.  The library never
 // allocates device memory and never synchronises the caller's stream.
 #include <algorithm>
+#include <cfloat>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -581,7 +582,7 @@ tw_status adamw_step(const tw_adamw_tensor* tensors, int32_t count, const tw_ada
   const double scalars[] = {args->lr, args->beta1, args->beta2, args->eps};
   for (double v : scalars)
     if (!std::isfinite(v) || v < 0.0) return TW_ERR_INVALID_ARG;
-  if (args->beta1 >= 1.0 || args->beta2 >= 1.0 || (float)args->eps <= 0.f)
+  if (args->beta1 >= 1.0 || args->beta2 >= 1.0 || (float)args->eps < FLT_MIN)
     return TW_ERR_INVALID_ARG;
   if (!args->step_dev && args->step < 1) return TW_ERR_INVALID_ARG;
   const void* words[] = {args->lr_dev, args->step_dev, args->grad_scale};

@@ -22,8 +22,9 @@
 // 32 or 64 a CTA) were 2 to 20% slower, since a warp's loads do not overlap its
 // own arithmetic, and forcing six CTAs on an SM spilled registers.  Measured on the
 // three 8192 x 2048 matrices of a 2B layer: fp32 moments, fp32 masters and
-// gradients, bf16 weights (30 bytes an element) 225 us, 6.7 TB/s; 8-bit moments, bf16
-// gradients, with the values written (20 bytes) 185 us, 5.4 TB/s.
+// gradients, bf16 weights (30 bytes an element) 223 us, 6.8 TB/s; 8-bit moments, bf16
+// gradients, with the values written (20 bytes) 170 us, 5.9 TB/s, there with three quarters
+// of the issue slots busy.
 //
 // The tensors' descriptors travel as kernel parameters: nothing has to stay
 // alive after the call and a captured step replays with them.
@@ -132,9 +133,16 @@ TW_DEV void store_codes(void* base, int64_t i, int valid, uint32_t w) {
     if (k < valid) static_cast<uint8_t*>(base)[i + k] = (uint8_t)(w >> (8 * k));
 }
 
+// The approximate instructions, values below 2^-126 as zero (their exact handling
+// was a seventh of the 8-bit form's instructions).
 TW_DEV float sqrt_approx(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+TW_DEV float reciprocal_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -211,7 +219,7 @@ TW_DEV void step_block(const Tensor& t, const Step& st, int64_t block, int lane)
       const float vn = v[h][k] = fmaf(st.b2, v[h][k], st.c2 * gs * gs);
       const float r = root[h][k] = SMALL ? sqrt_approx(vn) : sqrtf(vn);
       const float den = fmaf(r, st.rsqrt_bias2, st.eps);
-      const float q = SMALL ? __fdividef(mn, den) : __fdiv_rn(mn, den);
+      const float q = SMALL ? mn * reciprocal_approx(den) : __fdiv_rn(mn, den);
       p[h][k] = fmaf(p[h][k], st.keep, -st.size * q);
       // elements past n take no part in the block's maximum, whatever a
       // block scale of NaN made of them

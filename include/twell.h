@@ -439,9 +439,10 @@ TW_API tw_status norm_residual_backward(const tw_norm_block* b, const void* dn, 
  *              v uint8  c in [0, 255]     v = (v_scale * c * c)^2
  *            The scale puts the block's largest magnitude on the largest code;
  *            others go to the nearest code in the square root of the ratio,
- *            and a v that is not zero keeps a code that is not zero.  A NaN or
- *            infinite moment makes its whole block NaN; a block of m whose
- *            largest magnitude is below 2^-127 is held as zero.  All-zero
+ *            and a v of 2^-126 or more keeps a code that is not zero (less is
+ *            held as zero).  A NaN or infinite moment makes its whole block
+ *            NaN; a block of m whose largest magnitude is below 2^-127 is held
+ *            as zero.  All-zero
  *            codes and scales are the states of a first step.
  *   m_values, v_values
  *            state_bits 8 only, both or neither: receive what the new codes
@@ -488,7 +489,7 @@ typedef struct {
  * The parameter moves by the moments as computed; only what is kept of them is
  * rounded to 8 bits.  The descriptors travel in the launch, up to 32 tensors
  * in a small one and 256 in a large one; longer lists take several launches.
- * `tensors` is read during the call only.  0 <= beta < 1, eps > 0.  Tensors
+ * `tensors` is read during the call only.  0 <= beta < 1, eps >= 2^-126.  Tensors
  * with n == 0 are skipped and their pointers may be NULL.  No written array may
  * overlap another array of the list (TW_ERR_INVALID_ARG): the same parameter
  * twice in one step has no defined order.

@@ -78,7 +78,7 @@ def test_refusals(L):
     assert L.adamw_step(None, 1, None, None) == INVALID
     assert _call(L, _desc(), count=-1) == INVALID
     for bad in (dict(lr=-1.0), dict(lr=float("nan")), dict(b1=1.0), dict(b2=-0.1), dict(eps=0.0),
-                dict(eps=1e-60), dict(step=0)):
+                dict(eps=1e-60), dict(eps=1e-39), dict(step=0)):
         assert _call(L, _desc(), **bad) == INVALID
     assert _call(L, _desc(), step_dev=FAKE + 2) == ALIGN
     assert _call(L, _desc(n=-1)) == INVALID
