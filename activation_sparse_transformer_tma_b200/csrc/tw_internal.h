@@ -140,7 +140,8 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
 // Workspace for dividing the reductions of y and dx (`split`), 0 where they are not.
 size_t gated_forward_split_bytes(int T, int d, int F);
 size_t gated_backward_split_bytes(int T, int d, int F);
-// The same forward for few tokens (gated_few.cu).
+// The same forward for few tokens (gated_few.cu), up to where the tile kernels take over
+// (2048 x 8192: 96 tokens 36.6 us against 40, 128 tokens 41.4 against 40).
 constexpr int kGatedFewMaxT = 112;
 cudaError_t launch_gated_few(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
                              int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z, uint16_t* u,

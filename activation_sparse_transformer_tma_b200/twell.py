@@ -442,6 +442,12 @@ def _dtype_code(t):
         raise TypeError(f"unsupported dtype {t.dtype}") from None
 
 
+def _activation(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act is one of {sorted(ACTIVATIONS)}, not {act!r}")
+    return ACTIVATIONS[act]
+
+
 def _check_ffn(x, Wg_t, Wu_t, Wd):
     T, d = x.shape
     F = Wg_t.shape[0]
@@ -481,7 +487,7 @@ def gated_ffn_forward(x, Wg_t, Wu_t, Wd, act, y, ws, z=None, u=None, dev_status=
     for t in (z, u):
         if t is not None and t.shape != (T, F):
             raise ValueError(f"z and u of {(T, F)} expected, got {tuple(t.shape)}")
-    _call_on(index, "gated_ffn_forward", stream, xp, gp, up, dp, T, d, F, ACTIVATIONS[act], zp, usp,
+    _call_on(index, "gated_ffn_forward", stream, xp, gp, up, dp, T, d, F, _activation(act), zp, usp,
              yp, _dtype_code(y), wsp, ws.numel() * ws.element_size(), sp)
 
 
@@ -499,7 +505,7 @@ def gated_ffn_backward(x, dy, Wg_t, Wu_t, Wd, act, z, u, dx, dWg_t, dWu_t, dWd, 
         raise ValueError(f"z and u of {(T, F)} expected")
     if dWg_t.dtype != dWu_t.dtype or dWg_t.dtype != dWd.dtype:
         raise TypeError("the weight gradients differ in dtype")
-    _call_on(index, "gated_ffn_backward", stream, xp, dyp, gp, up, dp, T, d, F, ACTIVATIONS[act],
+    _call_on(index, "gated_ffn_backward", stream, xp, dyp, gp, up, dp, T, d, F, _activation(act),
              zp, usp, dxp, _dtype_code(dx), dgp, dup, ddp, _dtype_code(dWg_t), wsp,
              ws.numel() * ws.element_size(), sp)
 

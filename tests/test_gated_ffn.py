@@ -130,6 +130,8 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError):
         twell.gated_ffn_forward(x, w, w, w, "silu", x, x)    # not on a GPU
     with pytest.raises(ValueError):
+        twell._activation("tanh")
+    with pytest.raises(ValueError):
         twell._check_ffn(x, w, w, w[:64])
     with pytest.raises(TypeError):
         twell._check_ffn(x.float(), w, w, w)

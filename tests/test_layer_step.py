@@ -192,3 +192,68 @@ def test_captured_steps_replay_with_new_inputs():
             assert torch.equal(A.master[k], B.master[k]) and torch.equal(A.w[k], B.w[k])
         for k in A.vec:
             assert torch.equal(A.vec[k], B.vec[k])
+
+
+@pytest.mark.parametrize("T", [1, 20, 112, 113, 300])
+def test_calls_queued_back_to_back_equal_separate_ones(T):
+    """Optimiser steps, forwards and backwards on shared workspaces, nothing waiting between them:
+    each call sees the weights that the step before it wrote, bit for bit as with a wait after
+    every call."""
+    def run(wait):
+        L = Layer(T, 256, 512, "silu", 11)
+        out = []
+        for s in range(1, 5):
+            L.forward_backward()
+            out += [t.clone() for t in (L.y, L.n, L.dr_in, *L.grad.values())]
+            L.update(step=s)
+            if wait:
+                torch.cuda.synchronize()
+            twell.gated_ffn_forward(L.x, L.w["Wg"], L.w["Wu"], L.w["Wd"], L.act, L.y, L.ws)
+            out.append(L.y.clone())
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert int(L.status) == 0
+        return out + [v.clone() for v in L.w.values()]
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_few_tokens_captured_with_an_optimiser_step_between(T):
+    """The few-token kernels read a weight before the kernel in front of them has ended: not
+    before the optimiser step that wrote it."""
+    A, B = (Layer(T, 256, 1024, "gelu_tanh" if T == 3 else "relu", 5) for _ in range(2))
+
+    def steps(L):
+        for _ in range(3):
+            L.forward_backward()
+            L.update(step_dev=L.step)
+            twell.gated_ffn_forward(L.x, L.w["Wg"], L.w["Wu"], L.w["Wd"], L.act, L.y, L.ws)
+
+    steps(B)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps(A)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(A.y, B.y)
+    for k in A.w:
+        assert torch.equal(A.w[k], B.w[k])
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    A, B, C, D = (Layer(T, 128, 256, "silu", T) for T in (40, 200, 40, 200))
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        for L, s in zip((A, B), streams):
+            with torch.cuda.stream(s):
+                L.forward_backward()
+    torch.cuda.synchronize()
+    C.forward_backward(), D.forward_backward()
+    torch.cuda.synchronize()
+    for L, M in ((A, C), (B, D)):
+        assert torch.equal(L.n, M.n) and all(torch.equal(L.grad[k], M.grad[k]) for k in L.grad)
