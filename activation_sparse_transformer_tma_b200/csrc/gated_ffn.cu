@@ -180,9 +180,19 @@ TW_DEV void slab_read(uint32_t slab, int lane, uint32_t (&w)[16]) {
                  : "r"(slab_chunk(slab, lane, q)) : "memory");
 }
 
+// An fp32 row of a double slab: 32 columns, 128 bytes, 128-byte swizzle.
+TW_DEV void slab_write_f32(uint32_t slab, int lane, const uint32_t (&w)[32]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(slab + lane * 128 + ((q ^ (lane & 7)) << 4)), "r"(w[4 * q]),
+                   "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3]) : "memory");
+}
+
 struct Maps {
   CUtensorMap a[3], b[3];
   CUtensorMap e[5];  // of the epilogue, boxes of 32 columns x 32 rows
+  CUtensorMap o[4];  // results, the same boxes
 };
 
 // ------------------------------------------------------------------- tiles --
@@ -484,17 +494,22 @@ TW_DEV void store_bf16(uint16_t* dst, const uint32_t (&w)[16], int left) {
           make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
 }
 
-// Plain results [M][N], rounded once to bf16 or stored in fp32.  Long reductions
-// leave time for plain stores.
+// Plain results [M][N], rounded once to bf16 or stored in fp32: 32 x 32 at a time
+// through two slabs in turns (fp32: one of twice the size).  Stores of a row a lane
+// straight from registers left short reductions bound by the epilogue.
+struct StoreState {
+  int turn;
+};
 template <class Ops>
 struct EpiStore : Ops {
   int M, N;
   bool bf16;
   void* out[3];
+  int first_map;     // maps.o of its first product
   float* parts;      // partial sums and arrival counters of a divided reduction
   uint32_t* arrived;
-  struct State {};
-  TW_DEV void begin(State&, const EpiWarp&, const Maps&, const Tiles&) const {}
+  using State = StoreState;
+  TW_DEV void begin(State& s, const EpiWarp&, const Maps&, const Tiles&) const { s.turn = 0; }
   // 32 columns of this lane's row.
   TW_DEV void store(const Tile& t, int row, int col, const uint32_t (&r)[32]) const {
     if (row >= M) return;
@@ -571,54 +586,76 @@ struct EpiStore : Ops {
       if (col0 + c * 32 < N) store(t, w.row0(t) + w.lane, col0 + c * 32, r);
     }
   }
-  TW_DEV bool run(State&, const EpiWarp& w, const Maps&, const Tiles& tiles, uint32_t taddr,
+  TW_DEV bool run(State& s, const EpiWarp& w, const Maps& maps, const Tiles& tiles, uint32_t taddr,
                   const Tile& t, int index) const {
     if (tiles.splits > 1) {
       join(w, tiles, taddr, t, index);
       return true;
     }
-    const int row = w.row0(t) + w.lane, part = t.width / 2;
+    const int row0 = w.row0(t), part = t.width / 2;
+    if (row0 >= M) return true;  // uniform over the warp, as all conditions below
+    const CUtensorMap* to = &maps.o[first_map + t.product];
 #pragma unroll 1
     for (int c = w.half * part; c < w.half * part + part; c += 32) {
       const int col = t.col + c;
-      if (col >= N) break;  // uniform
+      if (col >= N) break;
       uint32_t r[32];
       __syncwarp();
       tmem_ld_32x32b_x32(taddr + c, r);
+      // the last stores from this slab have read it
+      if (w.lane == 0) {
+        if (bf16) stores_read<1>();
+        else stores_read<0>();
+      }
+      __syncwarp();
       tmem_ld_wait();
-      store(t, row, col, r);
+      const uint32_t slab = w.slab(bf16 ? s.turn : 0);
+      if (bf16) {
+        uint32_t v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        slab_write(slab, w.lane, v);
+      } else {
+        slab_write_f32(slab, w.lane, r);
+      }
+      fence_async_proxy();
+      __syncwarp();
+      if (w.lane == 0) {  // rows and columns past the end are not stored
+        tma_store(to, slab, col, row0);
+        stores_commit();
+      }
+      s.turn ^= 1;
     }
     return true;
   }
-  TW_DEV void end(State&, const EpiWarp&) const {}
+  TW_DEV void end(State&, const EpiWarp& w) const {
+    if (w.lane == 0) stores_done();
+  }
 };
-using OpsDown = Operands<false, false, true, false, false, 6, 0>;
-using OpsDx = Operands<false, false, true, true, false, 6, 0>;
-using OpsGrads = Operands<false, true, true, false, true, 6, 0>;
+using OpsDown = Operands<false, false, true, false, false, 6, 2>;
+using OpsDx = Operands<false, false, true, true, false, 6, 2>;
+using OpsGrads = Operands<false, true, true, false, true, 6, 2>;
 
 // dx and the weight gradients in one launch, where dx has few tiles: the weight
 // gradients fill the pairs that it leaves idle (a step of 1003 tokens, d = 1024, F = 4096:
 // 106.6 -> 102.7 us).  Operands of the weight gradients:
 // a[2] and e[2] (dWd), e[0] and e[3] (dWu), e[1] and e[3] (dWg).
-struct EpiInputs : Operands<false, false, true, true, false, 6, 0> {
+struct EpiInputs : Operands<false, false, true, true, false, 6, 2> {
   static constexpr bool kMixed = true;
   using Set = LeadTiles;
   EpiStore<OpsDx> dx;
   EpiStore<OpsGrads> grads;
-  struct State {};
-  TW_DEV void begin(State&, const EpiWarp&, const Maps&, const LeadTiles&) const {}
-  TW_DEV bool run(State&, const EpiWarp& w, const Maps& maps, const LeadTiles& tiles,
+  using State = StoreState;
+  TW_DEV void begin(State& s, const EpiWarp&, const Maps&, const LeadTiles&) const { s.turn = 0; }
+  TW_DEV bool run(State& s, const EpiWarp& w, const Maps& maps, const LeadTiles& tiles,
                   uint32_t taddr, const Tile& t, int index) const {
-    if (t.product == 0) {
-      EpiStore<OpsDx>::State s;
-      return dx.run(s, w, maps, tiles.lead, taddr, t, index);
-    }
+    if (t.product == 0) return dx.run(s, w, maps, tiles.lead, taddr, t, index);
     Tile one = t;
     --one.product;
-    EpiStore<OpsGrads>::State s;
     return grads.run(s, w, maps, tiles.rest, taddr, one, index - tiles.lead.count);
   }
-  TW_DEV void end(State&, const EpiWarp&) const {}
+  TW_DEV void end(State& s, const EpiWarp& w) const { dx.end(s, w); }
 };
 
 // ------------------------------------------------------------------- kernel --
@@ -883,6 +920,11 @@ bool map_slab(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
   return make_tmap_bf16_sw64(m, base, rows, cols, 32);
 }
 
+bool map_result(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, bool bf16) {
+  return bf16 ? make_tmap_bf16_sw64(m, base, rows, cols, 32)
+              : make_tmap_f32(m, base, rows, cols, 32);
+}
+
 int div_up(int a, int b) { return a / b + (a % b != 0); }
 
 }  // namespace
@@ -920,7 +962,7 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
   if (!map_k(&m1.a[0], x, T, d) || !map_k(&m1.b[0], Wg_t, F, d) || !map_k(&m1.b[1], Wu_t, F, d) ||
       !map_slab(&m1.e[0], h, T, F) || (z && !map_slab(&m1.e[1], z, T, F)) ||
       (z && !map_slab(&m1.e[2], u, T, F)) || !map_k(&m2.a[0], h, T, F) ||
-      !map_mn(&m2.b[0], Wd, F, d))
+      !map_mn(&m2.b[0], Wd, F, d) || !map_result(&m2.o[0], y, T, d, y_dtype == TW_BF16))
     return cudaErrorInvalidValue;
   const Tiles t1 = plan_tiles(div_up(T, 2 * kBM), div_up(F, 128), 1, div_up(d, kBK), false);
   const Tiles t2 = down_tiles(T, d, F);
@@ -939,6 +981,7 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
   e2.N = d;
   e2.bf16 = y_dtype == TW_BF16;
   e2.out[0] = e2.out[1] = e2.out[2] = y;
+  e2.first_map = 0;
   e2.arrived = static_cast<uint32_t*>(split);
   e2.parts = reinterpret_cast<float*>(static_cast<char*>(split) + counter_bytes(t2));
   return launch_pairs(m2, t2, e2, status, stream);
@@ -958,8 +1001,11 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
       !map_mn(&m3.a[2], dz, T, F) || !map_mn(&m3.b[0], dy, T, d) || !map_mn(&m3.b[1], x, T, d) ||
       !map_mn(&m3.b[2], x, T, d) || !map_slab(&m1.e[0], h, T, F) || !map_slab(&m1.e[1], z, T, F) ||
       !map_slab(&m1.e[2], u, T, F) || !map_slab(&m1.e[3], du, T, F) ||
-      !map_slab(&m1.e[4], dz, T, F))
+      !map_slab(&m1.e[4], dz, T, F) || !map_result(&m2.o[0], dx, T, d, dx_dtype == TW_BF16))
     return cudaErrorInvalidValue;
+  void* const grads[3] = {dWd, dWu_t, dWg_t};
+  for (int i = 0; i < 3; ++i)
+    if (!map_result(&m3.o[i], grads[i], F, d, dw_dtype == TW_BF16)) return cudaErrorInvalidValue;
   EpiBackward e1;
   e1.T = T;
   e1.F = F;
@@ -977,15 +1023,15 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
   e2.N = d;
   e2.bf16 = dx_dtype == TW_BF16;
   e2.out[0] = e2.out[1] = e2.out[2] = dx;
+  e2.first_map = 0;
   e2.arrived = static_cast<uint32_t*>(split);
   e2.parts = reinterpret_cast<float*>(static_cast<char*>(split) + counter_bytes(t2));
   EpiStore<OpsGrads> e3;
   e3.M = F;
   e3.N = d;
   e3.bf16 = dw_dtype == TW_BF16;
-  e3.out[0] = dWd;
-  e3.out[1] = dWu_t;
-  e3.out[2] = dWg_t;
+  for (int i = 0; i < 3; ++i) e3.out[i] = grads[i];
+  e3.first_map = 0;
   e3.arrived = nullptr;
   e3.parts = nullptr;
   Tiles t3 = plan_tiles(div_up(F, 2 * kBM), nd, 3, div_up(T, kBK), true);
@@ -1008,6 +1054,9 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
     EpiInputs e4;
     e4.dx = e2;
     e4.grads = e3;
+    e4.grads.first_map = 1;
+    m.o[0] = m2.o[0];
+    for (int i = 0; i < 3; ++i) m.o[1 + i] = m3.o[i];
     return launch_pairs(m, both, e4, status, stream);
   }
   e = launch_pairs(m2, t2, e2, status, stream);

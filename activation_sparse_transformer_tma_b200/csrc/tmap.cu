@@ -24,15 +24,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-bool encode(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
-            uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+bool encode(CUtensorMap* m, CUtensorMapDataType type, uint32_t size, const void* base,
+            uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
+            CUtensorMapSwizzle swizzle) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
+  cuuint64_t strides[1] = {cols * size};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box,
             es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -41,12 +42,20 @@ bool encode(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint
 
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                     uint32_t box_cols, uint32_t box_rows) {
-  return encode(m, base, rows, cols, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols, box_cols, box_rows,
+                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool make_tmap_bf16_sw64(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows) {
-  return encode(m, base, rows, cols, 32, box_rows, CU_TENSOR_MAP_SWIZZLE_64B);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols, 32, box_rows,
+                CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+bool make_tmap_f32(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                   uint32_t box_rows) {
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, rows, cols, 32, box_rows,
+                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace tw

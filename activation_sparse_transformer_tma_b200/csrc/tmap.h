@@ -17,4 +17,8 @@ bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t co
 bool make_tmap_bf16_sw64(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows);
 
+// The same of a row-major fp32 matrix: boxes of 32 columns (128 bytes).
+bool make_tmap_f32(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                   uint32_t box_rows);
+
 }  // namespace tw
