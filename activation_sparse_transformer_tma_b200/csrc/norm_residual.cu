@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(fwd_threads(TEAM), TEAM <= 256 ? 2 : 1)
 // ----------------------------------------------------------------- backward --
 // Rows are dealt out in items: at most rows_per_item consecutive rows of one gate
 // group (per_group items cover a group).  An item belongs to a CTA, whose teams
-// share its rows, or to one team (by_team: with short groups, and where a CTA is one
+// share its rows, or to one team (by_team: short groups, and where a CTA is one
 // team); either way the gate row's gradient is complete, or one partial of
 // per_group, when the item is done.
 struct Items {
@@ -681,46 +681,51 @@ struct RowSum {
 };
 struct RowSums {
   RowSum s[3];
-  int first[4];  // prefix sums of the output rows
+  int first[4];  // prefix sums of the CTAs
   int count, d;
 };
 
-// 32 columns of one output row a CTA, its partial rows dealt over 16 warps and
-// their 16 sums added in order.
+// 32 columns of an output row each: by a CTA, its partial rows dealt over 16 warps and
+// their sums added in order, or, with few partial rows (a group's items), by a warp.
 constexpr int kSumWarps = 16;
+constexpr int kFewParts = 16;
 __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const RowSums a) {
   __shared__ float sums[kSumWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int strips = (a.d + 31) / 32;
-  const int at = blockIdx.x / strips, c = (blockIdx.x - at * strips) * 32 + lane;
   int i = 0;
-  while (i + 1 < a.count && at >= a.first[i + 1]) ++i;
+  while (i + 1 < a.count && (int)blockIdx.x >= a.first[i + 1]) ++i;
   const RowSum& s = a.s[i];
-  const int row = at - a.first[i];
+  const bool few = s.each <= kFewParts;
+  int unit = blockIdx.x - a.first[i];
+  if (few) unit = unit * kSumWarps + warp;
+  const int row = unit / strips, c = (unit - row * strips) * 32 + lane;
   pdl_wait();
   pdl_launch_next();
+  const int first = few ? 0 : warp, step = few ? 1 : kSumWarps;
   float v = 0.f;
-  if (c < a.d) {
+  if (row < s.rows && c < a.d) {
     const float* p = s.part + (size_t)row * s.each * a.d + c;
-    for (int k0 = warp; k0 < s.each; k0 += 8 * kSumWarps) {
+    for (int k0 = first; k0 < s.each; k0 += 8 * step) {
       float x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int k = k0 + j * kSumWarps;
+        const int k = k0 + j * step;
         x[j] = k < s.each ? p[(size_t)k * a.d] : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) v += x[j];
     }
   }
-  sums[warp][lane] = v;
-  __syncthreads();
-  if (warp == 0 && c < a.d) {
+  if (!few) {
+    sums[warp][lane] = v;
+    __syncthreads();
+    if (warp != 0) return;
     v = 0.f;
 #pragma unroll
     for (int k = 0; k < kSumWarps; ++k) v += sums[k][lane];
-    s.out[(size_t)row * a.d + c] = v;
   }
+  if (row < s.rows && c < a.d) s.out[(size_t)row * a.d + c] = v;
 }
 
 int team_size_of(int d) {
@@ -735,9 +740,9 @@ struct Plan {
   Items it;
   int ctas, threads, team;
 };
-// Groups shorter than this go to one team each: a CTA's teams would share too few
-// rows of one, and meet at a barrier after each.
-constexpr int kShortGroup = 32;
+// What an item costs beside its rows, in rows of one team: a team on its own stores its
+// sums, a CTA's teams meet twice and add theirs.
+constexpr int kTeamItem = 1, kCtaItem = 2;
 
 Plan make_plan(int T, int d, int gate_group, int sms) {
   Plan p;
@@ -748,20 +753,31 @@ Plan make_plan(int T, int d, int gate_group, int sms) {
   const int group = gate_group <= 0 || gate_group > T ? (T > 0 ? T : 1) : gate_group;
   const int groups = (int)((T64 + group - 1) / group);
   p.it.group = group;
-  const bool short_groups = group < kShortGroup && groups > 1;
-  p.it.by_team = short_groups || teams == 1;
-  if (short_groups) {
-    p.it.per_group = 1;
-    p.it.rows_per_item = group;
-  } else {
-    // one item for every SM, and no second wave for a few more; an item has a row
-    // for each team at least
-    long long per = groups >= sms ? 1 : sms / groups;
-    const long long most = (group + (long long)teams - 1) / teams;
-    if (per > most) per = most;
-    p.it.rows_per_item = (int)((group + per - 1) / per);
-    p.it.per_group = (int)((group + (long long)p.it.rows_per_item - 1) / p.it.rows_per_item);
+  // The rounds of items times their length: groups whole to a team each, or cut into `per`
+  // items for CTAs.  (8192 x 2048, groups of 31: 2 rounds of CTAs, where teams of their own
+  // took 87 us for the call; groups of 100: 5 items each, where whole groups on 82 of 148
+  // CTAs took 109.)
+  const long long teams_all = (long long)sms * teams;
+  long long best = groups > 1 ? (groups + teams_all - 1) / teams_all * ((long long)group + kTeamItem)
+                              : 0;
+  long long rows = group;
+  bool by_team = groups > 1;
+  const long long most = (group + (long long)teams - 1) / teams;  // a row for each team
+  for (long long rounds = 1; rounds <= 16; ++rounds) {
+    long long per = rounds * sms / groups;  // as many items as the rounds hold
+    per = per < 1 ? 1 : per > most ? most : per;
+    const long long length = (group + per - 1) / per, items = groups * ((group + length - 1) / length);
+    const long long cost = (items + sms - 1) / sms * ((length + teams - 1) / teams + kCtaItem);
+    if (best == 0 || cost < best) {
+      best = cost;
+      rows = length;
+      by_team = false;
+    }
+    if (per == most) break;
   }
+  p.it.by_team = by_team || teams == 1;
+  p.it.rows_per_item = (int)rows;
+  p.it.per_group = (int)((group + rows - 1) / rows);
   p.it.count = groups * p.it.per_group;
   const int units = (int)(p.it.by_team ? ((long long)p.it.count + teams - 1) / teams : p.it.count);
   p.ctas = units < sms ? units : sms;
@@ -936,16 +952,17 @@ cudaError_t launch_norm_backward(const tw_norm_block& b, const void* dn, const v
   s.first[0] = 0;
   auto add = [&](const float* part, float* out, int rows, int each) {
     s.s[s.count] = RowSum{part, out, rows, each};
-    s.first[s.count + 1] = s.first[s.count] + rows;
+    const long long units = (long long)rows * ((b.d + 31) / 32);
+    const long long ctas = each <= kFewParts ? (units + kSumWarps - 1) / kSumWarps : units;
+    s.first[s.count + 1] = s.first[s.count] + (int)ctas;
     ++s.count;
   };
   if (dw_pre) add(g.part_pre, dw_pre, 1, p.ctas);
   if (dw_post) add(g.part_post, dw_post, 1, p.ctas);
   if (gate_parts) add(g.dgate, dgate, p.it.count / p.it.per_group, p.it.per_group);
   if (s.count == 0) return cudaSuccess;
-  const unsigned strips = (unsigned)(b.d + 31) / 32;
-  return launch_pdl(norm_sum_kernel, dim3(strips * (unsigned)s.first[s.count]),
-                    dim3(kSumWarps * 32), 0, stream, s);
+  return launch_pdl(norm_sum_kernel, dim3((unsigned)s.first[s.count]), dim3(kSumWarps * 32), 0,
+                    stream, s);
 }
 
 }  // namespace tw

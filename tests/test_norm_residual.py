@@ -368,6 +368,18 @@ def test_backward(T, d, gate):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,d", [(2000, 64), (1500, 1000), (900, 2048), (60, 4104)])
+@pytest.mark.parametrize("group", [2, 12, 31, 50, 100, 333])
+def test_backward_of_groups_of_every_length(T, d, group):
+    """Groups to a team each, to a CTA each, and cut into several items."""
+    rng = np.random.default_rng(T + group)
+    t, got, run = _backward(rng, T, d, group, BF, F32, BF, BF, True, True, True)
+    run()
+    torch.cuda.synchronize()
+    _check_backward(t, got, group, 0.75, 0.5)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,d,group", [(50, 8192, 7), (90, 8192, 40), (300, 8192, 300), (90, 4096, 40),
                                        (90, 4096, 3), (200, 2048, 33), (90, 512, 40)])
 def test_all_fp32_with_gate_rows(T, d, group):
