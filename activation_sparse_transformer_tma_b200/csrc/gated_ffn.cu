@@ -26,9 +26,8 @@
 // PFLOP/s), a training step of 8192 tokens 2.01 to 2.09 ms.  In a loop the power cap
 // bounds the products (tensor pipe 97 to 98% active at 1.46 GHz).
 //
-// Every wait is bounded: on timeout
-// the CTA flags TW_ERR_TIMEOUT, stops its roles, lets its copies land and meets its
-// pair at the last barrier.
+// Every wait is bounded: on timeout the CTA flags TW_ERR_TIMEOUT, stops its roles, lets
+// its copies land and meets its pair at the last barrier.
 #include "tmap.h"
 #include "pdl.cuh"
 #include "cluster.cuh"
@@ -201,8 +200,8 @@ struct Maps {
 // to 16 rows measure alike at these sizes; the weights of larger ones leave L2).  When the
 // last round of tiles would leave half of the pairs idle, its tiles are cut into
 // two of 128 columns (`full` tiles before them; MN-major B only), each in about 0.75 of
-// a whole one's time.  A launch of few
-// tiles, all of them cut so, also divides the reduction into `splits`.
+// a whole one's time.  A launch of few tiles, all of them cut so, also divides the
+// reduction into `splits`.
 constexpr int kGroupM = 8;
 struct Tile {
   int product, m, col, width;  // tile row; first column (of units: dual B), columns
@@ -663,8 +662,7 @@ struct EpiInputs : Operands<false, false, true, true, false, 6, 2> {
 template <class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_gemm_kernel(const __grid_constant__ Maps maps, const typename Epi::Set tiles,
-                     const Epi epi,
-                     int32_t* status, unsigned long long timeout_ns) {
+                     const Epi epi, int32_t* status, unsigned long long timeout_ns) {
   constexpr int kStages = Epi::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -789,7 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // K-major: 16 k further along the swizzled row; MN-major: 16 k-rows
             // further, boxes of 64 columns 8 KB apart
             const uint64_t ad = amn ? sdesc_mnmajor_sw128(a + kk * 2048, kBK * 64 * 2)
-                                          : sdesc_kmajor_sw128(a + kk * 32);
+                                    : sdesc_kmajor_sw128(a + kk * 32);
             const uint64_t bd = Epi::kBMN ? sdesc_mnmajor_sw128(b + kk * 2048, kBK * 64 * 2)
                                           : sdesc_kmajor_sw128(b + kk * 32);
             umma_pair(d, ad, bd, idesc, kb != t.k0 || kk != 0 ? 1u : 0u);
@@ -928,9 +926,6 @@ bool map_result(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, 
 
 int div_up(int a, int b) { return a / b + (a % b != 0); }
 
-}  // namespace
-
-namespace {
 Tiles down_tiles(int T, int d, int F) {
   return plan_tiles(div_up(T, 2 * kBM), div_up(d, kBN), 1, div_up(F, kBK), true);
 }
@@ -943,6 +938,7 @@ bool too_large(int T, int d, int F) {
   const long long nf = div_up(F, 128), nd = div_up(d, kBN);
   return mt * nf > 0x3FFFFFFF || mt * nd > 0x3FFFFFFF || 3 * mf * nd > 0x3FFFFFFF;
 }
+
 }  // namespace
 
 size_t gated_forward_split_bytes(int T, int d, int F) {

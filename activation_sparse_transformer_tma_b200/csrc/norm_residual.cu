@@ -773,7 +773,8 @@ Plan make_plan(int T, int d, int gate_group, int sms) {
       rows = length;
       by_team = false;
     }
-    if (per == most) break;
+    // without gate rows a CTA has one item, whose partial row is the CTA's
+    if (per == most || groups == 1) break;
   }
   p.it.by_team = by_team || teams == 1;
   p.it.rows_per_item = (int)rows;
