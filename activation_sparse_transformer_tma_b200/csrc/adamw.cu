@@ -23,7 +23,7 @@
 // own arithmetic, and forcing six CTAs on an SM spilled registers.  Measured on the
 // three 8192 x 2048 matrices of a 2B layer: fp32 moments, fp32 masters and
 // gradients, bf16 weights (30 bytes an element) 223 us, 6.8 TB/s; 8-bit moments, bf16
-// gradients, with the values written (20 bytes) 166 to 171 us, 5.9 to 6.1 TB/s, with three quarters
+// gradients, with the values written (20 bytes) 166 to 173 us, 5.8 to 6.1 TB/s, with three quarters
 // of the issue slots busy.
 //
 // The tensors' descriptors travel as kernel parameters: nothing has to stay

@@ -1,7 +1,9 @@
 /*
  * twell.h -- C ABI of libtwell.so: the activation-sparse gated FFN of a
  * ReLU-gated transformer layer on one NVIDIA B200 (sm_100a), with the
- * activations carried in the Tile-wise ELLPACK ("TwELL") format.
+ * activations carried in the Tile-wise ELLPACK ("TwELL") format; and, for layers
+ * around or beside it, a dense gated FFN with a choice of activation, the norms before
+ * and after a block with its gate and residual sum, and a multi-tensor AdamW step.
  *
  * Method: technical summary page of "Sparser, Faster, Lighter Transformer
  * Language Models" (arXiv 2603.23198):
