@@ -351,11 +351,14 @@ struct BackwardArgs {
   float* part_pre;   // [CTAs][d]
 };
 
-// Shared memory behind the ring (byte offsets): w_pre in fp32; with gate rows, the sums
-// of dw_post over the items done (of a thread, or of the CTA's columns) and the teams'
-// sums of an item.  Sums over the teams behind the loop take the ring's place.
+// Shared memory behind the ring (byte offsets): w_pre in fp32; with gate rows, w_post in
+// fp32 where teams have their own items (-1 in the widest rows, which leave no room, and
+// for a CTA's items, too few to repay the copy: 8192 x 200 in groups of 31 takes 22.3 us
+// with it, 20.8 without), the sums of dw_post over the items done (of a thread, or of the
+// CTA's columns) and the teams' sums of an item.  Sums over the teams behind the loop
+// take the ring's place.
 struct Extra {
-  int wpre, post, comb;
+  int wpre, wpost, post, comb;
 };
 
 // Over an item the gate is one row, so one sum A = sum_t G yh serves both the gate
@@ -384,7 +387,8 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
   const int stride = it.by_team ? 1 : TEAMS;
   const uint32_t base = smem_u32(rows);
   const bool gate_rows = b.gate && it.group < b.T;
-  const bool gate_ring = gate_rows && ring.gate >= 0;
+  const bool gate_ring = TEAM <= 256 && gate_rows && ring.gate >= 0;
+  const bool wpost_kept = TEAM <= 256 && extra.wpost >= 0;
   zero_past<N>(base, ring, ring.y, b.y_bf16, tm.in);
   zero_past<N>(base, ring, ring.r, b.r_bf16, tm.in);
   zero_past<N>(base, ring, ring.gate, b.w_bf16, tm.in);
@@ -393,8 +397,9 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
   pdl_wait();
   pdl_launch_next();
 
+  auto group_of = [&](int item) { return it.per_group == 1 ? item : item / it.per_group; };
   auto range = [&](int item, int& row0, int& row1) {
-    const int group = item / it.per_group, part = item - group * it.per_group;
+    const int group = group_of(item), part = item - group * it.per_group;
     // group * it.group < T, so only the ends can pass T (and, added up, 2^31)
     const long long g0 = (long long)group * it.group;
     const long long g1 = g0 + it.group < b.T ? g0 + it.group : b.T;
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
       if (g.y) copy_row<TEAM, N>(to + ring.y, g.y, b.y_bf16, i, tm.in);
       if (gate_ring && ahead_new)
         copy_row<TEAM, N>(to + ring.gate, b.gate, b.w_bf16,
-                       (size_t)((int)ahead_item / it.per_group) * b.d + 4 * tm.tid, tm.in);
+                       (size_t)group_of((int)ahead_item) * b.d + 4 * tm.tid, tm.in);
       if (g.rstd_post) copy_float(to + ring.p + threadIdx.x * 4, g.rstd_post + ahead_row);
       if (g.rstd_pre) copy_float(to + ring.p + (N + threadIdx.x) * 4, g.rstd_pre + ahead_row);
       ahead_new = false;
@@ -487,14 +492,29 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
   };
 
   const bool keep_post = g.part_post && gate_rows;
+  // every team writes the same values; a thread reads the columns that it wrote
   float4* wpre = reinterpret_cast<float4*>(rows + extra.wpre) + tm.tid;
-  if (b.w_pre) {
+  auto keep = [&](float4* to, const void* from) {
     float w[kQ][4] = {};
-    load_row<TEAM>(b.w_pre, b.w_bf16, 4 * tm.tid, tm.in, w);
-    // every team writes the same values; a thread reads the columns that it wrote
+    load_row<TEAM>(from, b.w_bf16, 4 * tm.tid, tm.in, w);
 #pragma unroll
-    for (int h = 0; h < kQ; ++h) wpre[h * TEAM] = vec4(w[h]);
-  }
+    for (int h = 0; h < kQ; ++h) to[h * TEAM] = vec4(w[h]);
+  };
+  if (b.w_pre) keep(wpre, b.w_pre);
+  float4* wpost = reinterpret_cast<float4*>(rows + extra.wpost) + tm.tid;
+  if (wpost_kept) keep(wpost, b.w_post);
+  auto read_wpost = [&](float (&w)[kQ][4]) {
+    ones(w);
+    if (wpost_kept) {
+#pragma unroll
+      for (int h = 0; h < kQ; ++h) {
+        const float4 o = wpost[h * TEAM];
+        w[h][0] = o.x; w[h][1] = o.y; w[h][2] = o.z; w[h][3] = o.w;
+      }
+    } else if (b.w_post) {
+      load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
+    }
+  };
   if (keep_post) {
 #pragma unroll
     for (int h = 0; h < kQ; ++h) *mine(extra.post, h) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -505,19 +525,19 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
     const int item = (int)next_item;
     int row0, row1;
     range(item, row0, row1);
-    const int group = item / it.per_group;
+    const int group = group_of(item);
     const size_t gate_at = (size_t)group * b.d + 4 * tm.tid;
     bool new_item = true;
+    uint32_t from = base;  // the stage of the row in hand
     for (long long row = (long long)row0 + first; row < row1; row += stride) {
       fetch(stage == 0 ? ring.stages - 1 : stage - 1);  // into the stage read before
       copies_wait(ring.stages);
-      const uint32_t from = base + stage * ring.bytes;
+      from = base + stage * ring.bytes;
       if (++stage == ring.stages) stage = 0;
       if (new_item && g.y) {
         float w[kQ][4];
-        ones(w);
+        read_wpost(w);
         ones(F);
-        if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
         if (gate_ring) read_row<N>(from + ring.gate, b.w_bf16, F);
         else if (b.gate) load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, F);
 #pragma unroll
@@ -599,10 +619,12 @@ __global__ void __launch_bounds__(bwd_threads(TEAM), 1)
       float* to = g.dgate + (size_t)(it.per_group == 1 ? group : item) * b.d;
       if (it.by_team) {
         float w[kQ][4], gt[kQ][4];
-        ones(w);
+        read_wpost(w);
         ones(gt);
-        if (b.w_post) load_row<TEAM>(b.w_post, b.w_bf16, 4 * tm.tid, tm.in, w);
-        load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, gt);
+        // an item of one row still has its gate row in the ring (8192 x 2048 with a gate
+        // row each: 92 us for the call, 109 with gate and w_post from global memory)
+        if (gate_ring && row1 - row0 == 1) read_row<N>(from + ring.gate, b.w_bf16, gt);
+        else load_row<TEAM>(b.gate, b.w_bf16, gate_at, tm.in, gt);
 #pragma unroll
         for (int h = 0; h < kQ; ++h) {
           if (keep_post) {
@@ -875,20 +897,23 @@ cudaError_t backward_team(const Block& k, const BackwardArgs& g, const Plan& p,
   const bool gate_rows = k.gate && p.it.group < k.T;
   const int vector = 4 * 4 * kQ * N;  // fp32 columns of every thread
   const int wpre = k.w_pre ? 4 * 4 * kQ * TEAM : 0;
+  const int wpost =
+      gate_rows && k.w_post && p.it.by_team && TEAM <= 256 ? 4 * 4 * kQ * TEAM : 0;
   const int post = gate_rows && g.part_post ? vector : 0;
   const int comb = gate_rows && !p.it.by_team ? vector : 0;
-  // the widest rows' gate rows are read when they are needed, not ahead: with fp32
-  // arrays they would not fit
+  // the widest rows' gate rows and w_post are read when they are needed, not ahead: with
+  // fp32 arrays they would not fit
   const Ring ring = make_ring(N, !g.y ? 0 : k.y_bf16 ? 2 : 4, g.dn ? r : 0,
                               g.dr_out ? r : 0, !g.dn ? 0 : k.n_bf16 ? 2 : 4,
                               gate_rows && TEAM <= 256 ? w : 0, true,
-                              kSmemSm - wpre - post - comb);
+                              kSmemSm - wpre - wpost - post - comb);
   // the last sums over the teams take the ring's place
   int at = ring.bytes * ring.stages;
   if (at < 2 * vector) at = 2 * vector;
   Extra x;
   x.wpre = at;
-  x.post = x.wpre + wpre;
+  x.wpost = wpost ? x.wpre + wpre : -1;
+  x.post = x.wpre + wpre + wpost;
   x.comb = x.post + post;
   at = x.comb + comb;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(norm_backward_kernel<TEAM>), at);

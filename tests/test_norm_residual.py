@@ -380,6 +380,21 @@ def test_backward_of_groups_of_every_length(T, d, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,d", [(5001, 64), (3001, 520), (1501, 1000), (901, 2048), (301, 4096), (301, 8192)])
+@pytest.mark.parametrize("group", [1, 2])
+def test_backward_of_many_short_groups(T, d, group):
+    """Several groups a team, each of one row, or of two and the last of one."""
+    rng = np.random.default_rng(T + group)
+    for yt, rt, nt, wt, post, pre, with_dr in [(BF, F32, BF, BF, True, True, True),
+                                               (F32, F32, F32, F32, True, True, True),
+                                               (BF, BF, BF, F32, False, True, True)]:
+        t, got, run = _backward(rng, T, d, group, yt, rt, nt, wt, post, pre, with_dr)
+        run()
+        torch.cuda.synchronize()
+        _check_backward(t, got, group, 0.75, 0.5)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,d,group", [(50, 8192, 7), (90, 8192, 40), (300, 8192, 300), (90, 4096, 40),
                                        (90, 4096, 3), (200, 2048, 33), (90, 512, 40)])
 def test_all_fp32_with_gate_rows(T, d, group):
