@@ -506,6 +506,7 @@ TW_DEV void store_bf16(uint16_t* dst, const uint32_t (&w)[16], int left) {
 // 2048 x 8192: 130 us against 112).
 struct StoreState {
   int turn;
+  bool wide;  // the newest store is fp32, out of both slabs
 };
 template <class Ops>
 struct EpiStore : Ops {
@@ -516,7 +517,10 @@ struct EpiStore : Ops {
   float* parts;      // partial sums and arrival counters of a divided reduction
   uint32_t* arrived;
   using State = StoreState;
-  TW_DEV void begin(State& s, const EpiWarp&, const Maps&, const Tiles&) const { s.turn = 0; }
+  TW_DEV void begin(State& s, const EpiWarp&, const Maps&, const Tiles&) const {
+    s.turn = 0;
+    s.wide = false;
+  }
   // 32 columns of this lane's row.
   TW_DEV void store(const Tile& t, int row, int col, const uint32_t (&r)[32]) const {
     if (row >= M) return;
@@ -609,11 +613,13 @@ struct EpiStore : Ops {
       uint32_t r[32];
       __syncwarp();
       tmem_ld_32x32b_x32(taddr + c, r);
-      // the last stores from this slab have read it
+      // The last stores from this slab have read it.  Where dx and the weight gradients share
+      // a launch, a bf16 chunk may follow an fp32 one, whose store reads both slabs.
       if (w.lane == 0) {
-        if (bf16) stores_read<1>();
+        if (bf16 && !s.wide) stores_read<1>();
         else stores_read<0>();
       }
+      s.wide = !bf16;
       __syncwarp();
       tmem_ld_wait();
       const uint32_t slab = w.slab(bf16 ? s.turn : 0);
@@ -646,7 +652,7 @@ using OpsGrads = Operands<false, true, true, false, true, 6, 2>;
 
 // dx and the weight gradients in one launch, where dx has few tiles: the weight
 // gradients fill the pairs that it leaves idle (a step of 1003 tokens, d = 1024, F = 4096:
-// 106.6 -> 102.7 us).  Operands of the weight gradients:
+// 106.6 -> 102.7 us).  Both write through the same slabs, each in its own type.  Operands of the weight gradients:
 // a[2] and e[2] (dWd), e[0] and e[3] (dWu), e[1] and e[3] (dWg).
 struct EpiInputs : Operands<false, false, true, true, false, 6, 2> {
   static constexpr bool kMixed = true;
@@ -654,7 +660,10 @@ struct EpiInputs : Operands<false, false, true, true, false, 6, 2> {
   EpiStore<OpsDx> dx;
   EpiStore<OpsGrads> grads;
   using State = StoreState;
-  TW_DEV void begin(State& s, const EpiWarp&, const Maps&, const LeadTiles&) const { s.turn = 0; }
+  TW_DEV void begin(State& s, const EpiWarp&, const Maps&, const LeadTiles&) const {
+    s.turn = 0;
+    s.wide = false;
+  }
   TW_DEV bool run(State& s, const EpiWarp& w, const Maps& maps, const LeadTiles& tiles,
                   uint32_t taddr, const Tile& t, int index) const {
     if (t.product == 0) return dx.run(s, w, maps, tiles.lead, taddr, t, index);
