@@ -485,7 +485,8 @@ tw_status norm_residual_forward(const tw_norm_block* b, const void* y, const voi
 }
 
 size_t norm_residual_backward_workspace_size(int32_t T, int32_t d, int32_t gate_group) {
-  if (T < 0 || d <= 0 || gate_group < 0) return 0;
+  // no tokens: nothing is summed; widths that the call refuses
+  if (T <= 0 || d <= 0 || d % 8 != 0 || d > tw::kNormMaxD || gate_group < 0) return 0;
   return tw::norm_backward_ws_bytes(T, d, gate_group);
 }
 

@@ -756,8 +756,8 @@ int team_size_of(int d) {
   return team;
 }
 
-// The backward's launch: CTAs, and how rows are dealt out.  The same rule sizes the
-// workspace, from T, d and gate_group alone (sms: the SMs of the current device).
+// The backward's launch: CTAs, and how rows are dealt out, for T > 0.  The same rule sizes
+// the workspace, from T, d and gate_group alone (sms: the SMs of the current device).
 struct Plan {
   Items it;
   int ctas, threads, team;
@@ -772,7 +772,7 @@ Plan make_plan(int T, int d, int gate_group, int sms) {
   p.threads = bwd_threads(p.team);
   const int teams = p.threads / p.team;
   const long long T64 = T;
-  const int group = gate_group <= 0 || gate_group > T ? (T > 0 ? T : 1) : gate_group;
+  const int group = gate_group <= 0 || gate_group > T ? T : gate_group;
   const int groups = (int)((T64 + group - 1) / group);
   p.it.group = group;
   // The rounds of items times their length: groups whole to a team each, or cut into `per`

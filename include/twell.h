@@ -415,7 +415,8 @@ TW_API tw_status norm_residual_forward(const tw_norm_block* b, const void* y, co
  * (same dtype); other overlaps are refused.
  * ws: at least norm_residual_backward_workspace_size(T, d, gate_group) bytes
  * (gate_group 0 without a gate), asked with the device current that runs the call; calls sharing
- * one workspace must not overlap on the device.
+ * one workspace must not overlap on the device.  The size is 0 with T == 0 and for sizes that the
+ * call refuses.
  */
 TW_API size_t norm_residual_backward_workspace_size(int32_t T, int32_t d, int32_t gate_group);
 TW_API tw_status norm_residual_backward(const tw_norm_block* b, const void* dn, const void* dr_out,
