@@ -448,9 +448,25 @@ def _activation(act):
     return ACTIVATIONS[act]
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _int32(*values):
+    """Refuses what ctypes would cut to 32 bits in silence."""
+    for v in values:
+        if not -_INT32_MAX <= v <= _INT32_MAX:
+            raise ValueError(f"{v} does not fit 32 bits")
+
+
+def _gate_group(group):
+    """T or more is one group: a sentinel past 32 bits stays one."""
+    return min(group, _INT32_MAX)
+
+
 def _check_ffn(x, Wg_t, Wu_t, Wd):
     T, d = x.shape
     F = Wg_t.shape[0]
+    _int32(T, d, F)
     for w in (Wg_t, Wu_t, Wd):
         if w.shape != (F, d):
             raise ValueError(f"weights of {tuple(w.shape)} and {(F, d)} for rows of {d}")
@@ -459,10 +475,12 @@ def _check_ffn(x, Wg_t, Wu_t, Wd):
 
 
 def gated_ffn_workspace_size(T, d, F):
+    _int32(T, d, F)
     return int(lib().gated_ffn_workspace_size(T, d, F))
 
 
 def gated_ffn_backward_workspace_size(T, d, F):
+    _int32(T, d, F)
     return int(lib().gated_ffn_backward_workspace_size(T, d, F))
 
 
@@ -514,6 +532,8 @@ def _norm_block(T, d, y_dtype, r_dtype, n_dtype, weights, addresses, gate_group,
                 block_scale, eps):
     """The shared descriptor of a norm call; weights and addresses of (w_post, gate, w_pre)."""
     w_dtype = None
+    _int32(T, d)
+    gate_group = _gate_group(gate_group)
     for k, w in enumerate(weights):
         if w is None:
             continue
@@ -567,7 +587,8 @@ def norm_residual_forward(y, r, w_post, gate, w_pre, r_out, n_out, *, gate_group
 
 
 def norm_residual_backward_workspace_size(T, d, gate_group=0):
-    return int(lib().norm_residual_backward_workspace_size(T, d, gate_group))
+    _int32(T, d)
+    return int(lib().norm_residual_backward_workspace_size(T, d, _gate_group(gate_group)))
 
 
 def norm_residual_backward_workspace(T, d, gate_group=0, device="cuda"):
@@ -674,6 +695,7 @@ def adamw_step(tensors: AdamWTensors, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, s
     tensors of one element that a captured step reads at each replay."""
     if tensors.count == 0:
         return
+    _int32(step)
     for x, dtype in ((lr_dev, torch.float32), (step_dev, torch.int32),
                      (grad_scale, torch.float32)):
         if x is not None and (x.dtype != dtype or x.numel() != 1 or x.device != tensors.device):

@@ -24,6 +24,51 @@ def test_workspace_of_an_empty_batch_and_of_refused_sizes_is_empty(L, group):
         assert size(T, d, group) >= 2 * 4 * d, (T, d)
 
 
+@pytest.mark.parametrize("group", [4, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 63 - 1])
+def test_a_group_past_32_bits_is_one_group(group):
+    """Cut to 32 bits it would be another group: 2^32 + 1 a gate row per token, read past the one."""
+    f = torch.float32
+    b = twell._norm_block(4, 8, f, f, f, (None, torch.zeros(1, 8), None), (None, None, None), group,
+                          1.0, 1.0, 0.0)
+    assert b.gate_group >= 4
+    assert (twell.norm_residual_backward_workspace_size(10, 64, group + 6) ==
+            twell.norm_residual_backward_workspace_size(10, 64, 10))
+
+
+def test_sizes_past_32_bits_are_refused():
+    f = torch.float32
+    big = 2 ** 32 + 1
+    with pytest.raises(ValueError):
+        twell._norm_block(big, 8, f, f, f, (None, None, None), (None, None, None), 0, 1.0, 1.0, 0.0)
+    for sizes in ((big, 64, 64), (1, big, 64), (1, 64, big)):
+        with pytest.raises(ValueError):
+            twell.gated_ffn_workspace_size(*sizes)
+        with pytest.raises(ValueError):
+            twell.gated_ffn_backward_workspace_size(*sizes)
+    with pytest.raises(ValueError):
+        twell.norm_residual_backward_workspace_size(big, 64)
+    some = twell.AdamWTensors([])
+    some.count = 1
+    with pytest.raises(ValueError):
+        twell.adamw_step(some, lr=1e-3, step=2 ** 32 + 5)
+
+
+@pytest.mark.gpu
+def test_one_gate_row_for_a_group_past_32_bits():
+    T, d = 5, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    y, r = (torch.randn(T, d, generator=g, device="cuda") for _ in range(2))
+    gate = torch.randn(1, d, generator=g, device="cuda")
+    outs = []
+    for group in (T, 2 ** 32 + 1):
+        out = torch.empty_like(r)
+        twell.norm_residual_forward(y, r, None, gate, None, out, None, gate_group=group)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert torch.equal(*outs)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("group", [0, 1, 5])
 def test_backward_of_an_empty_batch_with_the_workspace_it_asks_for(group):
