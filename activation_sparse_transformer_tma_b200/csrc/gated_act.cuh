@@ -38,7 +38,9 @@ TW_DEV void activate(float z, float& a, float& da) {
     const float p =
         __fdividef(1.f, 1.f + __expf(-1.5957691f * z * fmaf(0.044715f * z, z, 1.f)));
     a = z * p;
-    da = fmaf(z * p * (1.f - p), 1.5957691f * fmaf(0.134145f * z, z, 1.f), p);
+    // far out p (1 - p) is zero, and z^2 must not be infinite beside it
+    const float t = fminf(fabsf(z), 1e9f);
+    da = fmaf(z * p * (1.f - p), 1.5957691f * fmaf(0.134145f * t, t, 1.f), p);
   }
 }
 

@@ -95,3 +95,30 @@ def test_derivatives_value_by_value(act):
         else:
             tol = H * np.abs(da) + (1 + _f64(z) ** 2) * 2.0 ** -18
         assert (np.abs(got_dz - da) - tol).max() <= 0
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T", [40, 200])
+def test_gates_far_out_saturate(act, T):
+    """z^2 passes fp32's range: act is z or 0 and act' 1 or 0, not a product of 0 and infinity."""
+    d = F = 256
+    ws = twell.gated_ffn_workspace(T, d, F, training=True)
+    far = torch.tensor([1e3, 1e10, 1e19, 1e20, 3e38, -1e3, -1e10, -1e19, -1e20, -3e38],
+                       device="cuda").repeat(F // 10 + 1)[:F].to(BF)
+    eye = torch.eye(F, d, device="cuda").to(BF)
+    x = torch.zeros(T, d, device="cuda", dtype=BF)
+    x[:, 0], x[:, 1] = 1.0, 1.0
+    Wg, Wu = (torch.zeros(F, d, device="cuda", dtype=BF) for _ in range(2))
+    Wg[:, 0], Wu[:, 1] = far, 1.0
+    y = torch.empty(T, d, device="cuda")
+    twell.gated_ffn_forward(x, Wg, Wu, eye, act, y, ws)
+    a, da = _exact(act, _f64(far))
+    assert np.array_equal(_f64(y), np.broadcast_to(a, (T, d)))
+    z, u = far.repeat(T, 1), torch.ones(T, F, device="cuda").to(BF)
+    one = torch.ones(T, d, device="cuda").to(BF)
+    x = torch.eye(T, d, device="cuda").to(BF)
+    dx = torch.empty(T, d, device="cuda")
+    dWg, dWu, dWd = (torch.empty(F, d, device="cuda") for _ in range(3))
+    twell.gated_ffn_backward(x, one, eye, eye, eye, act, z, u, dx, dWg, dWu, dWd, ws)
+    assert np.array_equal(_f64(dWg)[:, :T].T, np.broadcast_to(da, (T, F)))
+    assert np.array_equal(_f64(dWu)[:, :T].T, np.broadcast_to(a, (T, F)))
