@@ -11,7 +11,6 @@ adding less than 2^-14.  Over 32 x 32 elements the mean square of independent er
 by a few in a hundred, and that of the values by as much: 2 * 2^-8 is twice what a patch can
 be off, and one element that is wrong by its own size puts 1/32 = 8 * 2^-8 into its patch.
 """
-import numpy as np
 import pytest
 import torch
 
@@ -105,3 +104,85 @@ def test_dx_and_weight_gradients_of_different_types_in_one_launch(T, d, F):
             for got, want in zip(dW, dW32 if wt == F32 else dW16):
                 assert torch.equal(got, want)
     assert int(st) == 0
+
+
+# On 148 SMs (74 pairs), in tiles of gate-up, y, dh and dx:
+#   (2100, 2568, 2608)  189, 99, 99, 99: several a pair in all four products, nine tile rows, whole
+#                       and halved tiles of y and dx, dx and the weight gradients apart
+#   (2100, 1280, 640)   45, 45, 27, 45: whole tiles alone, one a pair, dx apart
+#   (5000, 136, 1032)   180, 40 halves, 100, 40 halves: several a pair, twenty tile rows
+#   (3000, 264, 2104)   204, 48, 108, 48: halves, and weight gradients by pairs that had a tile of dx
+#   (260, 4104, 1032)   18, 68, 10, 68: wide rows, weight gradients whole and halved
+STEPS = [(2100, 2568, 2608), (2100, 1280, 640), (5000, 136, 1032), (3000, 264, 2104),
+         (260, 4104, 1032)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,F", STEPS)
+def test_steps_of_many_tiles(T, d, F):
+    a = _inputs(T, d, F, T + d * F)
+    x, dy, Wg, Wu, Wd = a
+    ws = twell.gated_ffn_workspace(T, d, F, training=True)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    X, _, G, U, D = (t.double() for t in a)
+    z64, u64 = X @ G.T, X @ U.T
+    y64 = (_silu(z64)[0] * u64) @ D
+    want = None
+    for dtype in (BF, F32):
+        z, u = (torch.full((T + 1, F), 7.0, dtype=BF, device="cuda") for _ in range(2))
+        y, y0 = (torch.full((T + 1, d), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+        twell.gated_ffn_forward(x, Wg, Wu, Wd, "silu", y0[:T], ws, dev_status=st)
+        ws.fill_(255)                                       # what a workspace held does not matter
+        twell.gated_ffn_forward(x, Wg, Wu, Wd, "silu", y[:T], ws, z=z[:T], u=u[:T], dev_status=st)
+        assert torch.equal(y, y0)
+        for name, got, exact in (("z", z, z64), ("u", u, u64), ("y", y, y64)):
+            assert (got[T:] == 7).all()
+            _near(name, got[:T], exact)
+        if want is None:
+            want = _gradients(a, z[:T], u[:T])
+        for dw_dtype in (BF, F32):
+            dx = torch.full((T + 1, d), 7.0, dtype=dtype, device="cuda")
+            dW = [torch.full((F + 1, d), 7.0, dtype=dw_dtype, device="cuda") for _ in range(3)]
+            ws.fill_(255)
+            _backward(a, "silu", z[:T], u[:T], dx[:T], [w[:F] for w in dW], ws, st)
+            assert (dx[T:] == 7).all() and all((w[F:] == 7).all() for w in dW)
+            _near("dx", dx[:T], want[0])
+            for k in range(3):
+                _near(("dWg", "dWu", "dWd")[k], dW[k][:F], want[1][k])
+    assert int(st) == 0
+
+
+# one token's NaN or infinity: few tokens, tiles, divided reductions, several tiles a pair
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,F", [(40, 264, 520), (300, 264, 1032), (130, 512, 4096),
+                                   (2100, 520, 1032)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_token_that_is_not_finite_stays_alone(T, d, F, value):
+    a = _inputs(T, d, F, 3 * T)
+    x, dy, Wg, Wu, Wd = a
+    ws = twell.gated_ffn_workspace(T, d, F, training=True)
+    bad, rest = T - 3, torch.arange(T, device="cuda") != T - 3
+
+    def step(x, dy, z=None, u=None):
+        y, dx = (torch.empty((T, d), device="cuda") for _ in range(2))
+        dW = [torch.empty((F, d), device="cuda") for _ in range(3)]
+        if z is None:
+            z, u = (torch.empty((T, F), dtype=BF, device="cuda") for _ in range(2))
+            twell.gated_ffn_forward(x, Wg, Wu, Wd, "silu", y, ws, z=z, u=u)
+        _backward((x, dy, Wg, Wu, Wd), "silu", z, u, dx, dW, ws, None)
+        return y, z, u, dx, dW
+
+    y, z, u, dx, dW = step(x, dy)
+    xn = x.clone()
+    xn[bad, 5] = value
+    yn, zn, un, dxn, _ = step(xn, dy)
+    for got, want in ((yn, y), (zn, z), (un, u), (dxn, dx)):
+        assert torch.equal(got[rest], want[rest])
+    assert not torch.isfinite(yn[bad]).any()
+    dyn = dy.clone()
+    dyn[bad, 7] = value
+    _, _, _, dxn, dWn = step(x, dyn, z, u)
+    assert torch.equal(dxn[rest], dx[rest]) and not torch.isfinite(dxn[bad]).any()
+    col = torch.arange(d, device="cuda") != 7
+    assert torch.equal(dWn[2][:, col], dW[2][:, col])       # dWd: that column of dy alone
+    assert not torch.isfinite(dWn[2][:, 7]).any()
