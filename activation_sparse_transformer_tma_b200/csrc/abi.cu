@@ -592,7 +592,9 @@ tw_status adamw_step(const tw_adamw_tensor* tensors, int32_t count, const tw_ada
   // no exception may leave a C entry
   try {
     std::vector<AdamwRange> ranges;
-    ranges.reserve(9 * (size_t)count);
+    ranges.reserve(9 * (size_t)count + 3);
+    for (const void* w : words)  // four bytes each, read while the arrays are written
+      if (w) ranges.push_back({reinterpret_cast<uintptr_t>(w), reinterpret_cast<uintptr_t>(w) + 4, false});
     for (int32_t i = 0; i < count; ++i) {
       tw_status st = check_adamw_tensor(tensors[i], &ranges);
       if (st != TW_OK) return st;

@@ -494,8 +494,8 @@ typedef struct {
  * in a small one and 256 in a large one; longer lists take several launches.
  * `tensors` is read during the call only.  0 <= beta < 1, eps >= 2^-126.  Tensors
  * with n == 0 are skipped and their pointers may be NULL.  No written array may
- * overlap another array of the list (TW_ERR_INVALID_ARG): the same parameter
- * twice in one step has no defined order.
+ * overlap another array of the list or hold a device word of args
+ * (TW_ERR_INVALID_ARG): the same parameter twice in one step has no defined order.
  */
 TW_API tw_status adamw_step(const tw_adamw_tensor* tensors, int32_t count,
                             const tw_adamw_args* args, cudaStream_t stream);
