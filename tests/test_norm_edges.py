@@ -83,3 +83,71 @@ def test_backward_of_an_empty_batch_with_the_workspace_it_asks_for(group):
                                  e.clone() if group else None, dw[1], ws, gate_group=group)
     torch.cuda.synchronize()
     assert (dw == 0).all()
+
+
+def _case(T, d, group, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def normal(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+    f = torch.float32
+    c = dict(y=normal(T, d), r=normal(T, d, dtype=f), dn=normal(T, d), dr=normal(T, d, dtype=f),
+             gate=normal(-(-T // group), d), w_post=normal(d), w_pre=normal(d))
+    return c
+
+
+def _both(c, group, over_dn=False):
+    """All outputs of a forward and of the backward behind it."""
+    T, d = c["r"].shape
+    o = dict(r_out=torch.empty_like(c["r"]), n_out=torch.empty_like(c["y"]),
+             p=torch.empty(T, device="cuda"), q=torch.empty(T, device="cuda"))
+    twell.norm_residual_forward(c["y"], c["r"], c["w_post"], c["gate"], c["w_pre"], o["r_out"],
+                                o["n_out"], gate_group=group, rstd_post=o["p"], rstd_pre=o["q"])
+    dn = c["dn"].clone()
+    o.update(dy=dn if over_dn else torch.empty_like(c["y"]), dr=torch.empty_like(c["r"]),
+             dw_post=torch.empty(d, device="cuda"), dw_pre=torch.empty(d, device="cuda"),
+             dgate=torch.empty(c["gate"].shape, device="cuda"))
+    ws = twell.norm_residual_backward_workspace(T, d, group)
+    ws.fill_(255)                                           # what a workspace held does not matter
+    twell.norm_residual_backward(dn, c["dr"], c["y"], o["r_out"], c["w_post"], c["gate"],
+                                 c["w_pre"], o["p"], o["q"], o["dy"], o["dr"], o["dw_post"],
+                                 o["dgate"], o["dw_pre"], ws, gate_group=group)
+    return o
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,group", [(9, 72, 1), (300, 264, 7), (1000, 2048, 300), (40, 8192, 40)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_token_that_is_not_finite_stays_alone(T, d, group, value):
+    c = _case(T, d, group)
+    want = _both(c, group)
+    bad = T // 2
+    rest = torch.arange(T, device="cuda") != bad
+    groups = torch.arange(c["gate"].shape[0], device="cuda") != bad // group
+    columns = torch.arange(d, device="cuda") != 5
+    per_row = ("r_out", "n_out", "p", "q", "dy", "dr")
+    for key in ("y", "r", "dn", "dr"):
+        e = dict(c, **{key: c[key].clone()})
+        e[key][bad, 5] = value
+        got = _both(e, group)
+        for k in per_row:
+            assert torch.equal(got[k][rest], want[k][rest]), (key, k)
+        assert torch.equal(got["dgate"][groups], want["dgate"][groups]), key
+        assert not torch.isfinite(got["dr" if key != "y" else "dy"][bad]).all(), key
+    # dn reaches the other columns of dw_pre through nothing
+    e = dict(c, dn=c["dn"].clone())
+    e["dn"][bad, 5] = value
+    got = _both(e, group)
+    assert torch.equal(got["dw_pre"][columns], want["dw_pre"][columns])
+    assert not torch.isfinite(got["dw_pre"][5])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,group", [(9, 72, 1), (700, 1000, 100), (40, 8192, 40)])
+def test_dy_over_dn(T, d, group):
+    c = _case(T, d, group, 1)
+    apart, over = _both(c, group), _both(c, group, over_dn=True)
+    for k in apart:
+        assert torch.equal(apart[k], over[k]), k
