@@ -599,9 +599,7 @@ def decode_leg(torch, tw, hbm):
         y = torch.empty((T, d), dtype=torch.float32, device="cuda")
         ws = tw.fused_workspace(T, d)
         sws = tw.small_batch_workspace(T, d, F) if T <= 64 else None
-        if T == 1:
-            Wd_dense = dev["Wd"].t().contiguous()  # the comparator's [d][F] down weight
-        hd = torch.empty((T, F), dtype=torch.bfloat16, device="cuda")
+        dws = tw.gated_ffn_workspace(T, d, F)
         yd = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
         td, tw_warm = [], []
         tg, tf, ts = [], [], []
@@ -619,11 +617,11 @@ def decode_leg(torch, tw, hbm):
                 e1[0].record()
                 tw.twell_ffn_small_batch(dev["x"], dev["Wg_t"], dev["Wu_t"], dev["Wd"], g, y, sws)
                 e1[1].record()
-            # the in-library dense bf16 FFN of the same tokens (streams Wg, Wu, Wd)
+            # the library's fastest dense bf16 FFN of the same tokens (streams Wg, Wu, Wd)
             cold()
             e2 = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
             e2[0].record()
-            tw.dense_ffn_forward(dev["x"], dev["Wg_t"], dev["Wu_t"], Wd_dense, hd, yd)
+            tw.gated_ffn_forward(dev["x"], dev["Wg_t"], dev["Wu_t"], dev["Wd"], "relu", yd, dws)
             e2[1].record()
             torch.cuda.synchronize()
             if it >= 5:
@@ -671,13 +669,13 @@ def decode_leg(torch, tw, hbm):
         md = float(np.median(td))
         dense_bytes = 3 * F * d * 2
         r["dense_comparator"] = {
-            "what": "dense_ffn_forward (tcgen05 GEMMs, bf16 h and y), cold L2",
+            "what": "gated_ffn_forward with ReLU (tcgen05, bf16 h and y), cold L2",
             "step_us": md * 1e3, "streamed_bytes": dense_bytes,
             "hbm_GBps": dense_bytes / (md * 1e-3) / 1e9,
             "sparse_speedup": md / (float(np.median(ts)) if ts else (mg + mf))}
         out[f"T{T}"] = r
-        del hd, yd
-    del flush, Wd_dense
+        del dws, yd
+    del flush
     return out
 
 
@@ -787,6 +785,19 @@ def training_leg(torch, tw, dist=None, world=1):
     dense_saved = tw.dense_ffn_train_saved_bytes(T, F)
     dense_ws = tw.dense_ffn_train_workspace_size(T, F)
     del dws
+
+    # the same step (without the L1 term) by the dense gated FFN with ReLU
+    z, u = (torch.empty((T, F), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    gws = tw.gated_ffn_workspace(T, d, F, training=True)
+
+    def gated_step_fn():
+        tw.gated_ffn_forward(dev["x"], dev["Wg_t"], dev["Wu_t"], dev["Wd"], "relu", y, gws, z=z,
+                             u=u, dev_status=dst)
+        tw.gated_ffn_backward(dev["x"], dev["dy"], dev["Wg_t"], dev["Wu_t"], dev["Wd"], "relu", z,
+                              u, dx, grads.dWg_t, grads.dWu_t, grads.dWd, gws, dev_status=dst)
+
+    gated_step = back_to_back_ms(torch, gated_step_fn)
+    del z, u, gws
     if world > 1:  # the slowest rank sets the step time
         tt = torch.tensor([step], device="cuda")
         dist.all_reduce(tt, op=dist.ReduceOp.MAX)
@@ -802,6 +813,9 @@ def training_leg(torch, tw, dist=None, world=1):
                      "flops_per_step": 9 * 2.0 * T * d * F,
                      "tflops": 9 * 2.0 * T * d * F / (dense_step * 1e-3) / 1e12,
                      "device_status": int(dst.item())},
+           "gated_ffn_relu": {"ms_per_step": gated_step,
+                              "tflops": 9 * 2.0 * T * d * F / (gated_step * 1e-3) / 1e12,
+                              "sparse_speedup": gated_step / step},
            "sparse_speedup_vs_dense": dense_step / step,
            "sparse_speedup_vs_dense_phases": sum(dms.values()) / phases_sum,
            "memory_bytes": {
@@ -868,25 +882,34 @@ def row_gather_rate(torch, tw, mat):
 
 
 def dense_leg(torch, tw, x, Wg, Wu, Wd, T, d, F, ms_sparse, args):
-    """The in-library dense bf16 FFN of the same shape (tcgen05, no cuBLAS)."""
+    """The in-library dense bf16 FFNs of the same shape (tcgen05, no cuBLAS): the comparator
+    with a CTA a tile, and the dense gated FFN with ReLU, whose tiles belong to CTA pairs."""
     Wd_dense = Wd.t().contiguous()
     h = torch.empty((T, F), dtype=torch.bfloat16, device="cuda")
     yd = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
-    for _ in range(3):
-        tw.dense_ffn_forward(x, Wg, Wu, Wd_dense, h, yd)
-    torch.cuda.synchronize()
+    gws = tw.gated_ffn_workspace(T, d, F)
     n = max(5, min(args.steps, 100))
-    a = torch.cuda.Event(enable_timing=True)
-    b = torch.cuda.Event(enable_timing=True)
-    a.record()
-    for _ in range(n):
-        tw.dense_ffn_forward(x, Wg, Wu, Wd_dense, h, yd)
-    b.record()
-    torch.cuda.synchronize()
-    ms = a.elapsed_time(b) / n
     flops = 2.0 * T * d * F * 3
-    return {"ms_per_step": ms, "tokens_per_s": T / (ms * 1e-3), "tflops": flops / (ms * 1e-3) / 1e12,
-            "sparse_speedup": ms / ms_sparse}
+
+    def measure(fn):
+        for _ in range(3):
+            fn()
+        torch.cuda.synchronize()
+        a = torch.cuda.Event(enable_timing=True)
+        b = torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(n):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        ms = a.elapsed_time(b) / n
+        return {"ms_per_step": ms, "tokens_per_s": T / (ms * 1e-3),
+                "tflops": flops / (ms * 1e-3) / 1e12, "sparse_speedup": ms / ms_sparse}
+
+    out = measure(lambda: tw.dense_ffn_forward(x, Wg, Wu, Wd_dense, h, yd))
+    out["gated_ffn_relu"] = measure(
+        lambda: tw.gated_ffn_forward(x, Wg, Wu, Wd, "relu", yd, gws))
+    return out
 
 
 def cpu_baseline_leg(w, y_gpu):
