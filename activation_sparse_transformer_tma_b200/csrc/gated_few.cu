@@ -14,8 +14,8 @@
 // so the result does not depend on timing.  The exchange takes the ring's place.
 //
 // Measured at d = 2048, F = 8192, weights not in L2 (100.7 MB, 15.6 us at the measured
-// copy rate): 1 token 24.5 us, 16: 25.3, 37: 29.2, 64: 31.4, 96: 36.6, 128: 41.4, where the
-// tile kernels take 40.
+// copy rate): 1 token 24.5 us, 16: 25.3, 37: 29.2, 64: 31.4, 96: 36.6 (4.1 to 2.8 TB/s); at 112
+// as long as the tile kernels.
 //
 // The second kernel is launched while the first runs (programmatic dependent
 // launch).  It starts to read Wd at once -- the

@@ -305,8 +305,9 @@ struct Turns {
 };
 
 // h = act(z) u from the unrounded z and u; with KEEP z and u are kept (bf16) for the
-// backward, through the same two slabs: a slab for each of the three left room for five
-// stages instead of six (step of 1003 tokens at 1024 x 4096: 98.4 us, now 97.0).
+// backward, through the same two slabs, which leaves the ring its six stages (a slab for
+// each of the three leaves five; the two measure alike: a step of 1003 tokens at 1024 x 4096
+// takes 97 to 104 us from one machine to the next).
 template <bool KEEP>
 struct EpiGateUp : Operands<true, false, false, false, false, 6, 2> {
   int T, F, act;

@@ -140,8 +140,14 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
 // Workspace for dividing the reductions of y and dx (`split`), 0 where they are not.
 size_t gated_forward_split_bytes(int T, int d, int F);
 size_t gated_backward_split_bytes(int T, int d, int F);
-// The same forward for few tokens (gated_few.cu), up to where the tile kernels take over
-// (2048 x 8192: 96 tokens 36.6 us against 40, 128 tokens 41.4 against 40).
+// The same forward for few tokens (gated_few.cu), up to where the tile kernels take over.
+// Few-token against tile kernels, us at 16 / 64 / 96 / 112 tokens, weights not in L2:
+//   512 x 2048    10.7 / 14.7 / 18.4 / 21.0 against 17.9 / 18.7 / 19.0 / 19.4
+//   1024 x 4096   13.9 / 18.2 / 22.8 / 25.1 against 24.5 / 25.4 / 25.7 / 26.2
+//   2048 x 2816   14.6 / 19.6 / 24.0 / 26.6 against 28.3 / 27.5 / 28.0 / 28.3
+//   2048 x 8192   24.3 / 29.7 / 34.9 / 37.3 against 37.4 / 35.9 / 36.3 / 36.8
+//   4096 x 11008  51.5 / 58.6 / 64.8 / 68.6 against 78.7 / 79.8 / 80.6 / 81.3
+//   2048 x 16384  40.5 / 46.2 / 53.9 / 56.5 against 61.2 / 54.9 / 55.6 / 56.2
 constexpr int kGatedFewMaxT = 112;
 cudaError_t launch_gated_few(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
                              int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z, uint16_t* u,

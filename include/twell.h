@@ -379,7 +379,8 @@ TW_API tw_status gated_ffn_backward(const void* x, const void* dy, const void* W
  *   without y there is no block (the first norm of a network): r' = r, r_out,
  *             w_post, gate and rstd_post are NULL and w_pre is not.
  * Limits: d % 8 == 0, 8 <= d <= 8192, T >= 0 (with T == 0 the arrays sized by T
- * may be NULL).
+ * may be NULL).  Squares are summed in fp32: a row whose sum of squares passes its
+ * range has an inverse norm of 0.
  */
 typedef struct {
   int32_t T, d, gate_group;
