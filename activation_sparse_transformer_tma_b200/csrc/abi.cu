@@ -44,9 +44,11 @@ cudaError_t set_smem_limit(const void* func, int bytes) {
 
 namespace {
 std::atomic<unsigned long long> g_withheld_gate_wait{0};
+std::atomic<unsigned long long> g_withheld_ffn_wait{0};
 }  // namespace
 
 unsigned long long take_withheld_gate_wait() { return g_withheld_gate_wait.exchange(0); }
+unsigned long long take_withheld_ffn_wait() { return g_withheld_ffn_wait.exchange(0); }
 
 }  // namespace tw
 
@@ -188,6 +190,10 @@ int32_t twell_version(void) { return 200; }
 
 void tw_test_withhold_next_gate_loads(uint64_t wait_limit_ns) {
   tw::g_withheld_gate_wait.store(wait_limit_ns > 0 ? wait_limit_ns : 1);
+}
+
+void tw_test_withhold_next_gated_ffn_loads(uint64_t wait_limit_ns) {
+  tw::g_withheld_ffn_wait.store(wait_limit_ns > 0 ? wait_limit_ns : 1);
 }
 
 tw_status twell_gate_gemm(const void* x, const void* Wg_t, int32_t T, int32_t d, int32_t F,

@@ -82,7 +82,7 @@ template <bool DOWN>
 __global__ void __launch_bounds__(kThreads, 1)
     gated_few_kernel(const __grid_constant__ CUtensorMap w0, const __grid_constant__ CUtensorMap w1,
                      const __grid_constant__ CUtensorMap tokens, const Few f, int32_t* status,
-                     unsigned long long timeout_ns) {
+                     unsigned long long timeout_ns, int withhold_loads) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto rows = [&](int i) {
         tma_load_2d(stage(i) + kWBytes, &tokens, &sm->full[i % f.stages], (k_first + i) * kBK, 0);
       };
-      const int early = n < f.stages ? n : f.stages;
+      // withhold_loads (a test of the bounded waits): nothing is issued
+      const int loads = withhold_loads ? 0 : n, early = loads < f.stages ? loads : f.stages;
       if (DOWN) {
         for (int i = 0; i < early; ++i) weights(i);
         pdl_wait();
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       pdl_launch_next();
       int i = early;
-      for (; i < n; ++i) {
+      for (; i < loads; ++i) {
         if (!mbar_wait(&sm->empty[i % f.stages], ((i / f.stages) & 1u) ^ 1u, abort, timeout_ns)) {
           *abort = 1;
           set_status(status, kStatusTimeout);
@@ -296,7 +297,8 @@ int cluster_of(int tiles, int kblocks) {
 
 template <bool DOWN>
 cudaError_t launch_few(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& tokens,
-                       Few f, int tiles, int32_t* status, cudaStream_t stream) {
+                       Few f, int tiles, unsigned long long withheld_wait_ns, int32_t* status,
+                       cudaStream_t stream) {
   f.N = (f.T + 15) / 16 * 16;
   f.stage_bytes = kWBytes + f.N * kBK * 2;
   // two CTAs on an SM, of one kernel or of both (1 token: 24.8 us; with a deeper ring and
@@ -328,14 +330,16 @@ cudaError_t launch_few(const CUtensorMap& w0, const CUtensorMap& w1, const CUten
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, gated_few_kernel<DOWN>, w0, w1, tokens, f, status,
-                            kWaitTimeoutNs);
+                            withheld_wait_ns ? withheld_wait_ns : kWaitTimeoutNs,
+                            withheld_wait_ns ? 1 : 0);
 }
 
 }  // namespace
 
 cudaError_t launch_gated_few(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
                              int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z, uint16_t* u,
-                             void* y, tw_dtype y_dtype, int32_t* status, cudaStream_t stream) {
+                             void* y, tw_dtype y_dtype, unsigned long long withheld_wait_ns,
+                             int32_t* status, cudaStream_t stream) {
   const uint32_t n = (uint32_t)((T + 15) / 16 * 16);
   CUtensorMap mx, mg, mu, mh, md;
   if (!make_tmap_bf16(&mx, x, T, d, kBK, n) || !make_tmap_bf16(&mg, Wg_t, F, d, kBK, kUnits) ||
@@ -352,11 +356,13 @@ cudaError_t launch_gated_few(const void* x, const void* Wg_t, const void* Wu_t, 
   f.y_bf16 = y_dtype == TW_BF16;
   f.width = F;
   f.kblocks = (d + kBK - 1) / kBK;
-  cudaError_t e = launch_few<false>(mg, mu, mx, f, (F + kUnits - 1) / kUnits, status, stream);
+  cudaError_t e = launch_few<false>(mg, mu, mx, f, (F + kUnits - 1) / kUnits, withheld_wait_ns,
+                                    status, stream);
   if (e != cudaSuccess) return e;
   f.width = d;
   f.kblocks = (F + kBK - 1) / kBK;
-  return launch_few<true>(md, md, mh, f, (d + kRows - 1) / kRows, status, stream);
+  return launch_few<true>(md, md, mh, f, (d + kRows - 1) / kRows, withheld_wait_ns, status,
+                          stream);
 }
 
 }  // namespace tw

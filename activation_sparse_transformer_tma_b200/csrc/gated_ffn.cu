@@ -679,7 +679,8 @@ struct EpiInputs : Operands<false, false, true, true, false, 6, 2> {
 template <class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_gemm_kernel(const __grid_constant__ Maps maps, const typename Epi::Set tiles,
-                     const Epi epi, int32_t* status, unsigned long long timeout_ns) {
+                     const Epi epi, int32_t* status, unsigned long long timeout_ns,
+                     int withhold_loads) {
   constexpr int kStages = Epi::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -724,7 +725,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------ TMA producer --
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = pair; tile < count && ok; tile += pairs) {
+      // withhold_loads (a test of the bounded waits): no operand is loaded
+      for (int tile = pair; tile < count && ok && !withhold_loads; tile += pairs) {
         const Tile t = tiles.at(tile, Epi::kStep);
         const int m0 = t.m * 2 * kBM + rank * kBM;
         // dual B: this CTA's weight, 128 units; otherwise its half of the columns
@@ -912,14 +914,16 @@ size_t split_bytes(const Tiles& t) {
 
 template <class Epi>
 cudaError_t launch_pairs(const Maps& maps, const typename Epi::Set& t, const Epi& epi,
-                         int32_t* status, cudaStream_t stream) {
+                         unsigned long long withheld_wait_ns, int32_t* status,
+                         cudaStream_t stream) {
   if (t.count == 0) return cudaSuccess;
   constexpr size_t smem = Layout<Epi>::kSmem;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(pair_gemm_kernel<Epi>), (int)smem);
   if (e != cudaSuccess) return e;
   const int pairs = t.count < most_pairs() ? t.count : most_pairs();
   return launch_pdl(pair_gemm_kernel<Epi>, dim3(2 * pairs), dim3(kThreads), smem, stream, maps, t,
-                    epi, status, kWaitTimeoutNs);
+                    epi, status, withheld_wait_ns ? withheld_wait_ns : kWaitTimeoutNs,
+                    withheld_wait_ns ? 1 : 0);
 }
 
 // K-major operand: boxes of 64 columns (k) x 128 rows.
@@ -970,8 +974,10 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
                                  uint16_t* u, void* y, tw_dtype y_dtype, void* split,
                                  int32_t* status, cudaStream_t stream) {
   if (too_large(T, d, F)) return cudaErrorInvalidValue;
+  const unsigned long long withheld = take_withheld_ffn_wait();
   if (T <= kGatedFewMaxT)
-    return launch_gated_few(x, Wg_t, Wu_t, Wd, T, d, F, act, h, z, u, y, y_dtype, status, stream);
+    return launch_gated_few(x, Wg_t, Wu_t, Wd, T, d, F, act, h, z, u, y, y_dtype, withheld, status,
+                            stream);
   Maps m1{}, m2{};
   if (!map_k(&m1.a[0], x, T, d) || !map_k(&m1.b[0], Wg_t, F, d) || !map_k(&m1.b[1], Wu_t, F, d) ||
       !map_slab(&m1.e[0], h, T, F) || (z && !map_slab(&m1.e[1], z, T, F)) ||
@@ -986,7 +992,7 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
     epi.act = act;
     epi.arrived = static_cast<uint32_t*>(split);
     epi.n_arrived = counters_of(t2);
-    return launch_pairs(m1, t1, epi, status, stream);
+    return launch_pairs(m1, t1, epi, withheld, status, stream);
   };
   cudaError_t e = z ? gate_up(EpiGateUp<true>{}) : gate_up(EpiGateUp<false>{});
   if (e != cudaSuccess) return e;
@@ -998,7 +1004,7 @@ cudaError_t launch_gated_forward(const void* x, const void* Wg_t, const void* Wu
   e2.first_map = 0;
   e2.arrived = static_cast<uint32_t*>(split);
   e2.parts = reinterpret_cast<float*>(static_cast<char*>(split) + counter_bytes(t2));
-  return launch_pairs(m2, t2, e2, status, stream);
+  return launch_pairs(m2, t2, e2, withheld, status, stream);
 }
 
 cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_t, const void* Wu_t,
@@ -1008,6 +1014,7 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
                                   void* dWu_t, void* dWd, tw_dtype dw_dtype, void* split,
                                   int32_t* status, cudaStream_t stream) {
   if (too_large(T, d, F)) return cudaErrorInvalidValue;
+  const unsigned long long withheld = take_withheld_ffn_wait();
   Maps m1{}, m2{}, m3{};
   if (!map_k(&m1.a[0], dy, T, d) || !map_k(&m1.b[0], Wd, F, d) || !map_k(&m2.a[0], du, T, F) ||
       !map_k(&m2.a[1], dz, T, F) || !map_mn(&m2.b[0], Wu_t, F, d) ||
@@ -1029,8 +1036,8 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
   e1.n_arrived = counters_of(t2);
   const int nd = div_up(d, kBN);
   cudaError_t e = launch_pairs(
-      m1, plan_tiles(div_up(T, 2 * kBM), div_up(F, kBN), 1, div_up(d, kBK), false), e1, status,
-      stream);
+      m1, plan_tiles(div_up(T, 2 * kBM), div_up(F, kBN), 1, div_up(d, kBK), false), e1, withheld,
+      status, stream);
   if (e != cudaSuccess) return e;
   EpiStore<OpsDx> e2;
   e2.M = T;
@@ -1071,11 +1078,11 @@ cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_
     e4.grads.first_map = 1;
     m.o[0] = m2.o[0];
     for (int i = 0; i < 3; ++i) m.o[1 + i] = m3.o[i];
-    return launch_pairs(m, both, e4, status, stream);
+    return launch_pairs(m, both, e4, withheld, status, stream);
   }
-  e = launch_pairs(m2, t2, e2, status, stream);
+  e = launch_pairs(m2, t2, e2, withheld, status, stream);
   if (e != cudaSuccess) return e;
-  return launch_pairs(m3, t3, e3, status, stream);
+  return launch_pairs(m3, t3, e3, withheld, status, stream);
 }
 
 }  // namespace tw

@@ -50,6 +50,8 @@ constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;
 // tw_test_withhold_next_gate_loads (0 if none), consumed by the next tile-GEMM
 // gate launch.
 unsigned long long take_withheld_gate_wait();
+// The same of tw_test_withhold_next_gated_ffn_loads, consumed by the next dense gated FFN call.
+unsigned long long take_withheld_ffn_wait();
 
 // tcgen05 bf16 gate GEMM with TwELL epilogue.  Shapes validated by caller.
 cudaError_t launch_gate_twell_tc(const void* x, const void* Wg_t, int T, int d, int F,
@@ -151,7 +153,8 @@ size_t gated_backward_split_bytes(int T, int d, int F);
 constexpr int kGatedFewMaxT = 112;
 cudaError_t launch_gated_few(const void* x, const void* Wg_t, const void* Wu_t, const void* Wd,
                              int T, int d, int F, tw_act act, uint16_t* h, uint16_t* z, uint16_t* u,
-                             void* y, tw_dtype y_dtype, int32_t* status, cudaStream_t stream);
+                             void* y, tw_dtype y_dtype, unsigned long long withheld_wait_ns,
+                             int32_t* status, cudaStream_t stream);
 cudaError_t launch_gated_backward(const void* x, const void* dy, const void* Wg_t, const void* Wu_t,
                                   const void* Wd, int T, int d, int F, tw_act act,
                                   const uint16_t* z, const uint16_t* u, uint16_t* h, uint16_t* du,

@@ -33,7 +33,8 @@ EXPORTS = ["twell_gate_gemm", "twell_fused_updown_workspace_size", "twell_fused_
            "gated_ffn_backward_workspace_size", "gated_ffn_backward",
            "norm_residual_forward", "norm_residual_backward_workspace_size",
            "norm_residual_backward", "adamw_step",
-           "tw_test_withhold_next_gate_loads", "tw_measure_row_gather", "tw_measure_stream_read", "tw_status_string",
+           "tw_test_withhold_next_gate_loads", "tw_test_withhold_next_gated_ffn_loads",
+           "tw_measure_row_gather", "tw_measure_stream_read", "tw_status_string",
            "twell_version"]
 
 
@@ -147,6 +148,8 @@ def lib():
                                  ctypes.POINTER(TwAdamwArgsC), vp]
         L.tw_test_withhold_next_gate_loads.argtypes = [ctypes.c_uint64]
         L.tw_test_withhold_next_gate_loads.restype = None
+        L.tw_test_withhold_next_gated_ffn_loads.argtypes = [ctypes.c_uint64]
+        L.tw_test_withhold_next_gated_ffn_loads.restype = None
         L.tw_measure_row_gather.argtypes = [vp, i32, i32, ctypes.c_int64, ctypes.c_uint32, vp,
                                             vp]
         L.tw_measure_row_gather.restype = st

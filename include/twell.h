@@ -513,6 +513,13 @@ TW_API tw_status adamw_step(const tw_adamw_tensor* tensors, int32_t count,
  */
 TW_API void tw_test_withhold_next_gate_loads(uint64_t wait_limit_ns);
 
+/*
+ * The same for the next gated_ffn_forward or gated_ffn_backward call with T > 0: its
+ * kernels load no operands, every CTA gives up after about wait_limit_ns and flags
+ * TW_ERR_TIMEOUT, and the call's outputs are not written.
+ */
+TW_API void tw_test_withhold_next_gated_ffn_loads(uint64_t wait_limit_ns);
+
 /* Human-readable name of a status code. */
 /* Measurement aid, not part of the FFN: the gathered-row rate of the fused
  * up + down projection's roofline.  n_gathers rows of the bf16 matrix
