@@ -469,7 +469,8 @@ def _gate_group(group):
 def _check_ffn(x, Wg_t, Wu_t, Wd):
     T, d = x.shape
     F = Wg_t.shape[0]
-    _int32(T, d, F)
+    if T > _INT32_MAX or d > _INT32_MAX or F > _INT32_MAX:
+        _int32(T, d, F)
     for w in (Wg_t, Wu_t, Wd):
         if w.shape != (F, d):
             raise ValueError(f"weights of {tuple(w.shape)} and {(F, d)} for rows of {d}")
@@ -535,8 +536,9 @@ def _norm_block(T, d, y_dtype, r_dtype, n_dtype, weights, addresses, gate_group,
                 block_scale, eps):
     """The shared descriptor of a norm call; weights and addresses of (w_post, gate, w_pre)."""
     w_dtype = None
-    _int32(T, d)
-    gate_group = _gate_group(gate_group)
+    if T > _INT32_MAX or d > _INT32_MAX or gate_group > _INT32_MAX:
+        _int32(T, d)
+        gate_group = _gate_group(gate_group)
     for k, w in enumerate(weights):
         if w is None:
             continue
@@ -698,7 +700,8 @@ def adamw_step(tensors: AdamWTensors, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, s
     tensors of one element that a captured step reads at each replay."""
     if tensors.count == 0:
         return
-    _int32(step)
+    if not 0 <= step <= _INT32_MAX:
+        _int32(step)
     for x, dtype in ((lr_dev, torch.float32), (step_dev, torch.int32),
                      (grad_scale, torch.float32)):
         if x is not None and (x.dtype != dtype or x.numel() != 1 or x.device != tensors.device):
